@@ -20,6 +20,9 @@ Entry points, by family:
   ``attn_bwd_workspace_bytes``;
 * sequence parallelism: ``attn_merge_partials`` and the ring driver in
   :mod:`exact_attention_100_b200.ring`;
+* serving over a paged 4-bit cache (:mod:`exact_attention_100_b200.kv4`): ``attn_kv_tables``,
+  ``attn_rope_axes``, ``attn_rope_axes_bwd``, ``attn_kv4_cache``, ``attn_kv4_append``,
+  ``attn_kv4_read``, ``attn_fwd_kv4``, ``attn_fwd_kv4_workspace_bytes``;
 * status: ``attn_device_status``, ``attn_status_string``, ``attn_num_kernel_launches``,
   ``attn_selftest_wait_timeout``, ``attn_noalloc_selftest_wait_timeout``, ``attn_shutdown``.
 """
@@ -123,6 +126,7 @@ def lib() -> ctypes.CDLL:
         L.attn_num_kernel_launches.restype = ctypes.c_ulonglong
         L.attn_shutdown.argtypes = []
         L.attn_shutdown.restype = None
+        kv4.declare(L)
         _lib = L
     return _lib
 
@@ -863,3 +867,8 @@ def attn_selftest_wait_timeout(stream=None) -> None:
 def attn_device_status(stream=None) -> int:
     """Synchronises the stream; returns and clears the device status word (0 = ATTN_OK)."""
     return int(lib().attn_device_status(_stream_ptr(stream)))
+
+
+from . import kv4  # noqa: E402  (it uses the helpers above)
+from .kv4 import (attn_fwd_kv4, attn_fwd_kv4_workspace_bytes, attn_kv4_append, attn_kv4_cache,  # noqa: E402,F401
+                  attn_kv4_read, attn_kv_tables, attn_rope_axes, attn_rope_axes_bwd)

@@ -12,6 +12,7 @@
 #include "attn_kernels.h"
 #include "attn_merge.h"
 #include "attn_selftest.h"
+#include "kv_kernels.h"
 
 namespace ea {
 cudaError_t setup_fwd_bf16_kernels();
@@ -68,6 +69,8 @@ int device_state(DeviceState** out) {
     if (ea::setup_fwd_fp8_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
     if (ea::setup_hadamard_quant_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
     if (ea::setup_bwd_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
+    if (ea::setup_kv_tables_kernel() != cudaSuccess) return ATTN_ERR_CUDA;
+    if (ea::setup_kv4_attn_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
     st.num_sms = sms;
     st.ready = true;
   }
@@ -179,6 +182,21 @@ void fill_params(ea::FwdParams& p, void* o, float* lse, int* status, int B, int 
 }
 
 }  // namespace
+
+namespace ea {
+
+int device_info(int* num_sms, int** status) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  *num_sms = st->num_sms;
+  *status = st->status;
+  return ATTN_OK;
+}
+
+void count_launches(int n) { g_launches.fetch_add(n); }
+
+}  // namespace ea
 
 extern "C" {
 

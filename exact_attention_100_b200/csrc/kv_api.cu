@@ -1,0 +1,270 @@
+// C ABI of the serving entry points (declared in include/attn_kv.h): argument checks and launches.
+// Every argument is checked before the first CUDA call, so a bad call returns a status without touching
+// the device.
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "../../include/attn_kv.h"
+#include "kv_kernels.h"
+
+namespace {
+
+constexpr long long kIntMax = 0x7FFFFFFFll;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A row or head stride: a positive multiple of 8 below 2^36; that of an extent-1 dimension is not used.
+bool stride_ok(long long* s, long long extent) {
+  if (extent == 1) *s = 8;
+  return *s > 0 && *s % 8 == 0 && *s < (1ll << 36);
+}
+
+bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+bool page_ok(int page) { return page >= 16 && page <= 4096 && page % 16 == 0; }
+
+// page, num_blocks and the cache pointer of every entry point that takes a cache
+bool cache_ok(const void* cache, int page, int num_blocks) {
+  return cache != nullptr && aligned(cache, 16) && page_ok(page) && num_blocks > 0 &&
+         static_cast<long long>(num_blocks) * page <= kIntMax;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_kv_tables(const int* lens, const int* new_lens, int* block_table, const int* free_blocks, const int* cursor,
+                   int* slots, int* positions, int* cu_seqlens, int* lens_out, int* cursor_out, int B, int width,
+                   int page, int n_free, int total, void* stream) {
+  if (!lens || !new_lens || !block_table || !cursor || !cu_seqlens || !lens_out || !cursor_out) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || B > ea::kTablesMaxRequests || width <= 0 || !page_ok(page) || n_free < 0 || total < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if ((n_free > 0 && !free_blocks) || (total > 0 && (!slots || !positions))) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(width) * page > kIntMax || static_cast<long long>(B) * width > kIntMax)
+    return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(block_table), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(cursor), static_cast<const void*>(slots),
+                        static_cast<const void*>(positions), static_cast<const void*>(cu_seqlens),
+                        static_cast<const void*>(lens_out), static_cast<const void*>(cursor_out)})
+    if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+  ea::TablesParams p{};
+  int sms = 0;
+  const int rc = ea::device_info(&sms, &p.status);
+  if (rc != ATTN_OK) return rc;
+  p.lens = lens;
+  p.new_lens = new_lens;
+  p.table = block_table;
+  p.free_blocks = free_blocks;
+  p.cursor = cursor;
+  p.slots = slots;
+  p.positions = positions;
+  p.cu = cu_seqlens;
+  p.lens_out = lens_out;
+  p.cursor_out = cursor_out;
+  p.B = B;
+  p.width = width;
+  p.page = page;
+  p.n_free = n_free;
+  p.total = total;
+  if (ea::launch_kv_tables(p, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  ea::count_launches(1);
+  return ATTN_OK;
+}
+
+int attn_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const float* cos, const float* sin,
+                   const int* positions, int B, int Hq, int Hk, int N, int d, int naxes, const int* sections,
+                   int n_pos, const long long* strides, int inverse, int in_dtype, int out_dtype, void* stream) {
+  if (!q || !q_out || (k == nullptr) != (k_out == nullptr) || !cos || !sin || !positions || !sections || !strides)
+    return ATTN_ERR_INVALID_ARG;
+  for (const void* t : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out),
+                        static_cast<const void*>(cos), static_cast<const void*>(sin)})
+    if (!aligned(t, 16)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || Hq <= 0 || N <= 0 || (k && Hk <= 0) || d <= 0 || n_pos <= 0 || naxes < 1 || naxes > ea::kRopeMaxAxes)
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > kIntMax || static_cast<long long>(Hq) + (k ? Hk : 0) > (1 << 20))
+    return ATTN_ERR_INVALID_ARG;
+  if ((inverse != 0 && inverse != 1) || (in_dtype != ATTN_BF16 && in_dtype != ATTN_FP32) ||
+      (out_dtype != ATTN_BF16 && out_dtype != ATTN_FP32))
+    return in_dtype == ATTN_E4M3 || out_dtype == ATTN_E4M3 ? ATTN_ERR_UNSUPPORTED : ATTN_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 1024) return ATTN_ERR_UNSUPPORTED;
+  ea::RopeParams p{};
+  long long half = 0;
+  for (int a = 0; a < naxes; ++a) {
+    if (sections[a] <= 0) return ATTN_ERR_INVALID_ARG;
+    half += sections[a];
+    if (2 * half > d) return ATTN_ERR_INVALID_ARG;
+    p.sec_end[a] = static_cast<int>(half);
+  }
+  if (half % 4 != 0) return ATTN_ERR_UNSUPPORTED;
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  for (int t = 0; t < (k ? 2 : 1); ++t) {
+    const int ext[3] = {B, t ? Hk : Hq, N};
+    bool same = true;
+    for (int i = 0; i < 3; ++i) {
+      long long x = strides[3 * t + i], y = strides[6 + 3 * t + i];
+      if (!stride_ok(&x, ext[i]) || !stride_ok(&y, ext[i])) return ATTN_ERR_INVALID_ARG;
+      p.xs[t][i] = x;
+      p.ys[t][i] = y;
+      same = same && x == y;
+    }
+    if (in[t] == out[t] && (!same || in_dtype != out_dtype)) return ATTN_ERR_INVALID_ARG;
+    p.x[t] = in[t];
+    p.y[t] = out[t];
+    p.H[t] = ext[1];
+  }
+  int sms = 0;
+  const int rc = ea::device_info(&sms, &p.status);
+  if (rc != ATTN_OK) return rc;
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.B = B;
+  p.N = N;
+  p.d = d;
+  p.half = static_cast<int>(half);
+  p.naxes = naxes;
+  p.n_pos = n_pos;
+  p.inverse = inverse;
+  if (ea::launch_rope_axes(p, in_dtype == ATTN_FP32, out_dtype == ATTN_FP32, sms, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
+    return ATTN_ERR_CUDA;
+  ea::count_launches(1);
+  return ATTN_OK;
+}
+
+unsigned long long attn_kv4_tile_bytes(int d) { return head_dim_ok(d) ? 18ull * d : 0ull; }
+
+int attn_kv4_append(const void* k, const void* v, void* cache, const int* slots, const signed char* signs, int T,
+                    int Hk, int d, int page, int num_blocks, const long long* strides, void* stream) {
+  if (!k || !v || !slots || !strides || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(signs, 16))
+    return ATTN_ERR_INVALID_ARG;
+  if (!cache_ok(cache, page, num_blocks)) return ATTN_ERR_INVALID_ARG;
+  if (T <= 0 || Hk <= 0 || static_cast<long long>(T) * Hk > kIntMax) return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  ea::Kv4CacheParams p{};
+  long long s[4];
+  for (int i = 0; i < 4; ++i) {
+    s[i] = strides[i];
+    if (!stride_ok(&s[i], i & 1 ? Hk : T)) return ATTN_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  const int rc = ea::device_info(&sms, &p.status);
+  if (rc != ATTN_OK) return rc;
+  p.k = k;
+  p.v = v;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.slots = slots;
+  p.signs = signs;
+  p.T = T;
+  p.Hk = Hk;
+  p.page = page;
+  p.num_blocks = num_blocks;
+  p.k_sn = s[0];
+  p.k_sh = s[1];
+  p.v_sn = s[2];
+  p.v_sh = s[3];
+  if (ea::launch_kv4_append(p, d, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  ea::count_launches(1);
+  return ATTN_OK;
+}
+
+int attn_kv4_read(const void* cache, const int* slots, void* k, void* v, int T, int Hk, int d, int page,
+                  int num_blocks, int out_dtype, void* stream) {
+  if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!cache_ok(cache, page, num_blocks)) return ATTN_ERR_INVALID_ARG;
+  if (T <= 0 || Hk <= 0 || static_cast<long long>(T) * Hk > kIntMax) return ATTN_ERR_INVALID_ARG;
+  if (out_dtype != ATTN_BF16 && out_dtype != ATTN_FP32)
+    return out_dtype == ATTN_E4M3 ? ATTN_ERR_UNSUPPORTED : ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  ea::Kv4CacheParams p{};
+  int sms = 0;
+  const int rc = ea::device_info(&sms, &p.status);
+  if (rc != ATTN_OK) return rc;
+  p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  p.slots = slots;
+  p.k_out = k;
+  p.v_out = v;
+  p.T = T;
+  p.Hk = Hk;
+  p.page = page;
+  p.num_blocks = num_blocks;
+  if (ea::launch_kv4_read(p, d, out_dtype == ATTN_FP32, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  ea::count_launches(1);
+  return ATTN_OK;
+}
+
+unsigned long long attn_fwd_kv4_workspace_bytes(int d, int num_sms) {
+  if (!head_dim_ok(d) || num_sms < 0 || num_sms > 4096) return 0;
+  if (num_sms == 0) {
+    int* status = nullptr;
+    if (ea::device_info(&num_sms, &status) != ATTN_OK) return 0;
+  }
+  return ea::kv4_attn_workspace_bytes(d, num_sms);
+}
+
+int attn_fwd_kv4(const void* q, const void* cache, const int* block_table, const int* seq_lens,
+                 const int* cu_seqlens_q, void* o, float* lse, void* workspace, const signed char* signs, int B,
+                 int Hq, int Hk, int total_q, int max_seqlen_q, int d, int page, int num_blocks, int width,
+                 const long long* strides, float scale, int causal, void* stream) {
+  if (!q || !block_table || !seq_lens || !o || !workspace || !strides) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(signs, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_seqlens_q, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (!cache_ok(cache, page, num_blocks)) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || total_q <= 0 || max_seqlen_q <= 0 || width <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(width) * page > kIntMax || static_cast<long long>(total_q) * Hq > kIntMax ||
+      static_cast<long long>(B) * Hk > kIntMax)
+    return ATTN_ERR_INVALID_ARG;
+  if (cu_seqlens_q == nullptr && (total_q != B || max_seqlen_q != 1)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  long long s[4];
+  for (int i = 0; i < 4; ++i) {
+    s[i] = strides[i];
+    if (!stride_ok(&s[i], i & 1 ? Hq : total_q)) return ATTN_ERR_INVALID_ARG;
+  }
+  ea::Kv4AttnParams p{};
+  int sms = 0;
+  const int rc = ea::device_info(&sms, &p.status);
+  if (rc != ATTN_OK) return rc;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.cu_q = cu_seqlens_q;
+  p.signs = signs;
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.q_sn = s[0];
+  p.q_sh = s[1];
+  p.o_sn = s[2];
+  p.o_sh = s[3];
+  p.B = B;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.G = Hq / Hk;
+  p.total_q = total_q;
+  p.max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
+  p.width = width;
+  p.page = page;
+  p.num_blocks = num_blocks;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 /
+                                    (signs != nullptr ? std::sqrt(static_cast<double>(d)) : 1.0));
+  p.causal = causal;
+  p.min_rows = 0;
+  p.max_rows = 0x7FFFFFFF;
+  int launches = 0;
+  if (ea::launch_kv4_attn(p, d, sms, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return ATTN_ERR_CUDA;
+  ea::count_launches(launches);
+  return ATTN_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,84 @@
+// Internal interface between the serving entry points (kv_api.cu) and their kernels.  Not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace ea {
+
+// From attn_api.cu: the current device's set-up (an attn_status), and the launch counter.
+int device_info(int* num_sms, int** status);
+void count_launches(int n);
+
+struct TablesParams {
+  const int* lens;
+  const int* new_lens;
+  int* table;
+  const int* free_blocks;
+  const int* cursor;
+  int* slots;
+  int* positions;
+  int* cu;
+  int* lens_out;
+  int* cursor_out;
+  int* status;
+  int B, width, page, n_free, total;
+};
+constexpr int kTablesMaxRequests = 8192;  // three integers per request in shared memory
+cudaError_t setup_kv_tables_kernel();
+cudaError_t launch_kv_tables(const TablesParams& p, int num_sms, cudaStream_t stream);
+
+constexpr int kRopeMaxAxes = 4;
+struct RopeParams {
+  const void* x[2];          // q, k
+  void* y[2];
+  long long xs[2][3];        // {sb, sh, sn}
+  long long ys[2][3];
+  const float* cos;
+  const float* sin;
+  const int* positions;
+  int* status;
+  int B, N, H[2], d, half, naxes, n_pos;
+  int sec_end[kRopeMaxAxes];  // running sums of the sections
+  int inverse;
+};
+cudaError_t launch_rope_axes(const RopeParams& p, bool in_f32, bool out_f32, int num_sms, cudaStream_t stream);
+
+struct Kv4CacheParams {
+  const void* k;
+  const void* v;
+  void* k_out;
+  void* v_out;
+  uint8_t* cache;
+  const int* slots;
+  const signed char* signs;
+  int* status;
+  int T, Hk, page, num_blocks;
+  long long k_sn, k_sh, v_sn, v_sh;
+};
+cudaError_t launch_kv4_append(const Kv4CacheParams& p, int d, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4CacheParams& p, int d, bool out_f32, cudaStream_t stream);
+
+struct Kv4AttnParams {
+  const void* q;
+  void* o;
+  float* lse;
+  const uint8_t* cache;
+  const int* table;
+  const int* lens;
+  const int* cu_q;           // nullptr: one query per request
+  const signed char* signs;
+  int* status;
+  uint8_t* ws;
+  long long q_sn, q_sh, o_sn, o_sh;
+  int B, Hq, Hk, G, total_q, max_q, width, page, num_blocks;
+  float scale_log2;          // softmax scale * log2 e (times 1 / sqrt d with the transform)
+  int causal;
+  int min_rows, max_rows;    // requests with min_rows < query length * G <= max_rows are this launch's
+};
+unsigned long long kv4_attn_workspace_bytes(int d, int num_sms);
+cudaError_t setup_kv4_attn_kernels();
+cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches);
+
+}  // namespace ea

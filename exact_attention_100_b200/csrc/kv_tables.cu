@@ -1,0 +1,183 @@
+// Block tables and slot maps of a serving step, from the requests' lengths.
+//
+// With held_b = ceil(len_b / page) and need_b = ceil((len_b + new_b) / page) - held_b, the blocks of
+// request b are free_blocks[cursor + E_b ...], E_b the sum of need over the requests before it, and its
+// tokens are rows cu_b = sum of new before it.  Both are running sums over the requests, so one launch
+// does everything: every block of threads scans all the requests (a few thousand integers) into
+// shared memory and then writes its share of the tokens and of the table.  A token finds its request by
+// a search in the running sums; the block of a new page comes straight from the free list, so no thread
+// reads a table entry that another one writes.
+//
+// Bound by latency: a launch, one pass of loads, a scan, one pass of stores (8 bytes per token).  One
+// block of threads serves small steps; larger ones spread the tokens over several.  Where the caller
+// has lens and the cursor updated in place, the blocks form one cluster of at most 8 and meet at its
+// barrier between reading and writing them; otherwise they need not meet.
+
+#include "attn_kernels.h"
+#include "kv_kernels.h"
+
+namespace ea {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, s);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams p) {
+  extern __shared__ int sm[];
+  int* cu = sm;               // [B + 1] first row of each request
+  int* len = sm + p.B + 1;    // [B] tokens held
+  int* first = len + p.B;     // [B] index in free_blocks of its first new block; -1: not served
+  __shared__ long long wsum[2][kWarps];
+  __shared__ int taken;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cursor0 = *p.cursor;
+  const bool cursor_ok = cursor0 >= 0 && cursor0 <= p.n_free;
+  bool bad = !cursor_ok;
+  if (tid == 0) taken = 0;
+  __syncthreads();
+  long long need0 = 0, new0 = 0;  // sums over the requests of earlier rounds
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    int l = 0, n = 0, need = 0;
+    bool ok = b < p.B;
+    if (ok) {
+      l = p.lens[b];
+      n = p.new_lens[b];
+      if (l < 0 || n < 0 || static_cast<long long>(l) + n > static_cast<long long>(p.width) * p.page) {
+        ok = false;
+        bad = true;
+        n = 0;
+      } else {
+        need = (l + n + p.page - 1) / p.page - (l + p.page - 1) / p.page;
+      }
+    }
+    long long a = warp_scan(need, lane), c = warp_scan(n, lane);
+    if (lane == 31) {
+      wsum[0][warp] = a;
+      wsum[1][warp] = c;
+    }
+    __syncthreads();
+    long long ra = 0, rc = 0;  // sums of whole warps: before this one, and of the round
+    for (int w = 0; w < kWarps; ++w) {
+      const long long x = wsum[0][w], y = wsum[1][w];
+      if (w < warp) {
+        a += x;
+        c += y;
+      }
+      ra += x;
+      rc += y;
+    }
+    a += need0;  // inclusive
+    c += new0;
+    if (b < p.B) {
+      if (ok && c > p.total && n > 0) {
+        ok = false;
+        bad = true;
+      }
+      if (need > 0 && (!cursor_ok || cursor0 + a > p.n_free)) ok = false;
+      const long long c0 = c - n;
+      cu[b] = static_cast<int>(c0 < p.total ? c0 : p.total);
+      len[b] = l;
+      first[b] = ok ? static_cast<int>(need > 0 ? cursor0 + a - need : 0) : -1;
+      if (ok && need > 0) atomicMax(&taken, static_cast<int>(a));
+      if (b == p.B - 1) cu[p.B] = static_cast<int>(c < p.total ? c : p.total);
+    }
+    need0 += ra;
+    new0 += rc;
+    __syncthreads();
+  }
+  if (bad && blockIdx.x == 0) atomicOr(p.status, kDevStatusBadSeqlens);
+
+  // every block of a cluster has read lens and cursor before any writes them (a launch with several
+  // clusters does not write in place)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= p.B; b += kThreads) p.cu[b] = cu[b];
+    for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = len[b] + (first[b] >= 0 ? cu[b + 1] - cu[b] : 0);
+    if (tid == 0) *p.cursor_out = cursor0 + taken;
+  }
+  // new table entries, one warp per request
+  for (int b = blockIdx.x * kWarps + warp; b < p.B; b += gridDim.x * kWarps) {
+    if (first[b] < 0) continue;
+    const int held = (len[b] + p.page - 1) / p.page;
+    const int need = (len[b] + cu[b + 1] - cu[b] + p.page - 1) / p.page - held;
+    for (int j = lane; j < need; j += 32)
+      p.table[static_cast<long long>(b) * p.width + held + j] = p.free_blocks[first[b] + j];
+  }
+  // slots and positions, four consecutive tokens per thread
+  const int rows = cu[p.B];
+  const long long step = 4ll * kThreads * gridDim.x;
+  for (long long t4 = 4ll * (blockIdx.x * kThreads + tid); t4 < p.total; t4 += step) {
+    int lo = 0, hi = p.B;  // cu[lo] <= t4 < cu[hi], or the tokens behind the last request
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= t4) lo = mid;
+      else hi = mid;
+    }
+    int b = lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long t = t4 + i;
+      if (t >= p.total) break;
+      int slot = -1, pos = 0;
+      if (t < rows) {
+        while (cu[b + 1] <= t) ++b;
+        pos = len[b] + static_cast<int>(t) - cu[b];
+        if (first[b] >= 0) {
+          const int held = (len[b] + p.page - 1) / p.page;
+          const int j = pos / p.page;
+          const int blk = j < held ? p.table[static_cast<long long>(b) * p.width + j] : p.free_blocks[first[b] + j - held];
+          if (blk < 0) atomicOr(p.status, kDevStatusBadSeqlens);
+          else slot = static_cast<int>(static_cast<unsigned>(blk) * static_cast<unsigned>(p.page)) + (pos - j * p.page);
+        }
+      }
+      p.slots[t] = slot;
+      p.positions[t] = pos;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t setup_kv_tables_kernel() {
+  return cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (3 * kTablesMaxRequests + 1) * static_cast<int>(sizeof(int)));
+}
+
+cudaError_t launch_kv_tables(const TablesParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = (3 * static_cast<size_t>(p.B) + 1) * sizeof(int);
+  const bool in_place = p.lens_out == p.lens || p.cursor_out == p.cursor;
+  // one block of threads per 2048 tokens (one round of its threads): every block repeats the scan, so
+  // more of them would only add work
+  const long long want = (static_cast<long long>(p.total) + 4 * kThreads - 1) / (4 * kThreads);
+  int grid = static_cast<int>(want < 1 ? 1 : want > num_sms ? num_sms : want);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  if (in_place) {
+    grid = grid > 4 ? 8 : grid > 2 ? 4 : grid;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kv_tables_kernel, p);
+}
+
+}  // namespace ea

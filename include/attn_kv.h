@@ -1,0 +1,166 @@
+/*
+ * exact_attention_100_b200 -- C ABI of serving over a paged key/value cache held in 4 bits
+ * (sm_100a).  Companion of attn.h: the status codes, element types, ownership, stream and error
+ * conventions stated there hold here too, and attn_device_status() reports what these kernels
+ * find wrong on the device.
+ *
+ * The order of one serving step:
+ *   attn_kv_tables     lengths of the requests -> new block-table entries, slots, positions
+ *   attn_rope_axes     Q and K rotated at those positions (one or more position axes)
+ *   attn_kv4_append    K and V of the new tokens quantised into their slots
+ *   attn_fwd_kv4       attention of the new queries over each request's cache
+ *
+ * The cache
+ *   One uint8 device tensor [num_blocks, Hk, page / 16, 18 d], contiguous, 16-byte aligned: a block
+ *   of `page` tokens (a multiple of 16, at most 4096) of every key/value head, cut into tiles of 16
+ *   tokens.  num_blocks * page < 2^31.  A tile's 18 d bytes:
+ *     [0, 8d)     codes of K          [8d, 16d)   codes of V
+ *     [16d, 17d)  (s, z) of K         [17d, 18d)  (s, z) of V
+ *   (s, z) are bfloat16 pairs [16 tokens][d / 64 groups][2]; the value of code u of a group of 64
+ *   consecutive dimensions is u * s + z (u = 0 .. 15).  Codes lie in planes of w = min(d, 128)
+ *   dimensions, [d / w planes][16 tokens][w / 2 bytes].  With n = w / 64 groups in a plane, dimension
+ *   64 g + r of a plane (r < 64) is, in K's row, nibble r & 1 (low first) of byte
+ *   8 n (r / 16) + 8 g + (r % 16) / 2, and in V's row of byte 4 n (r / 8) + 4 g + (r % 8) / 2: the
+ *   order in which the lanes of a warp take a row with one wide load each.
+ *   A slot is block * page + offset of a token in its block; slot -1 is no token.
+ *   4.5 bits are held per value.
+ */
+#ifndef EXACT_ATTENTION_100_B200_ATTN_KV_H
+#define EXACT_ATTENTION_100_B200_ATTN_KV_H
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * attn_kv_tables -- block tables and slot maps of one serving step from the requests' lengths.
+ *
+ *   lens         [B] int32: tokens that request b holds in the cache.
+ *   new_lens     [B] int32: tokens it adds in this step (0 or more).
+ *   block_table  [B, width] int32, read and written: entry [b, j] is the block of tokens
+ *                j * page .. j * page + page - 1.  Entries 0 .. ceil(lens[b] / page) - 1 are read as they
+ *                are; those up to ceil((lens[b] + new_lens[b]) / page) - 1 are written; the others are left.
+ *   free_blocks  [n_free] int32: ids of blocks; those before the cursor are taken.  May be NULL if n_free = 0.
+ *   cursor       [1] int32, 0 .. n_free.
+ *   slots        [total] int32, written: the slot of each new token, requests in order, -1 behind
+ *                the last one.
+ *   positions    [total] int32, written: lens[b] + i for token i of request b, 0 behind the last one.
+ *   cu_seqlens   [B + 1] int32, written: running sums of new_lens, the offsets attn_fwd_kv4 takes.
+ *   lens_out     [B] int32, written: lens + new_lens.  May be lens itself.
+ *   cursor_out   [1] int32, written: the cursor past the blocks taken.  May be cursor itself.
+ *   B            1 .. 8192;  width >= 1;  page a multiple of 16;  n_free >= 0;  total >= 0 (the host's bound
+ *                on the sum of new_lens; width * page, B * width < 2^31).
+ * Blocks are handed out in request order.  A request that needs more blocks than are left (after
+ * those before it) takes none: its slots are -1 and its lens_out is lens; the same holds for every
+ * later request that needs a block.  Its tokens keep their rows in cu_seqlens and positions.
+ * A request whose lengths are negative, pass the table's width or pass `total` is reported by
+ * attn_device_status() as ATTN_ERR_INVALID_ARG, is not served and (the first two) adds no rows; so
+ * is a cursor outside its range (no block is handed out) and a negative block id (slot -1).
+ * All pointers 4-byte aligned.  Apart from the two pairs named, no output may overlap another array.
+ */
+int attn_kv_tables(const int* lens, const int* new_lens, int* block_table, const int* free_blocks, const int* cursor,
+                   int* slots, int* positions, int* cu_seqlens, int* lens_out, int* cursor_out, int B, int width,
+                   int page, int n_free, int total, void* stream);
+
+/*
+ * attn_rope_axes -- rotary position embedding with one to four position axes (time, height, width).
+ *
+ *   q, k        logical [B, H, N, d] tensors (Hq and Hk heads), element (b, h, n, c) at
+ *               base + b*sb + h*sh + n*sn + c; k (with k_out) may be NULL.
+ *   q_out, k_out  the same shapes with their own strides, written; may be q and k themselves (then with
+ *               the same strides and type), else no overlap.
+ *   strides     HOST pointer to 12 int64 values {sb, sh, sn} of q, k, q_out, k_out, in elements, with the
+ *               rules of attn_fwd_strided (multiples of 8).
+ *   cos, sin    [n_pos, half] float32, position-major: row p holds the `half` angles of position p.
+ *   positions   [naxes, B, N] int32, each in 0 .. n_pos - 1.
+ *   sections    HOST pointer to naxes positive ints, sum = half: pairs 0 .. sections[0] - 1 turn with axis
+ *               0, the next sections[1] with axis 1, and so on.  half a multiple of 4, 2 * half <= d.
+ *   inverse     0: y_i = x_i cos - x_{i+half} sin, y_{i+half} = x_{i+half} cos + x_i sin, the angle of pair i
+ *               at [positions[axis(i), b, n], i]; dimensions from 2 * half on are copied.
+ *               1: the transpose (sin negated): takes the gradient of y to the gradient of x.
+ *   in_dtype, out_dtype   ATTN_BF16 or ATTN_FP32.  float32 arithmetic, each product and the sum rounded.
+ *   d           a multiple of 8, at most 1024.
+ * A position outside its range is reported by attn_device_status() as ATTN_ERR_INVALID_ARG; the pairs
+ * that would turn with it are not written.  Tensor pointers and tables 16-byte aligned, positions 4-byte.
+ */
+int attn_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const float* cos, const float* sin,
+                   const int* positions, int B, int Hq, int Hk, int N, int d, int naxes, const int* sections,
+                   int n_pos, const long long* strides, int inverse, int in_dtype, int out_dtype, void* stream);
+
+/* attn_kv4_tile_bytes -- 18 d, the bytes of a tile of 16 tokens of one key/value head; 0 for a d other
+ * than 64, 128 or 256. */
+unsigned long long attn_kv4_tile_bytes(int d);
+
+/*
+ * attn_kv4_append -- K and V of T tokens quantised to 4 bits and written to their slots.
+ *
+ *   k, v        [T, Hk, d] bf16, device; strides: HOST pointer to 4 int64 values {row, head} of k, then
+ *               v, in elements, positive multiples of 8 (the head stride of Hk = 1 is ignored).
+ *   cache       as above, written at the slots only.
+ *   slots       [T] int32, device: distinct, or -1 (that token is skipped).  A slot given twice ends up
+ *               with a mixture of the two tokens.
+ *   signs       d int8 entries +-1, device: K is replaced by (1/sqrt d) H_d (D k) (float32 butterflies of stride
+ *               1, 2, 4, ..., then one product with float32(1/sqrt d)).  NULL: K as it is.  V as it is always.
+ *   T, Hk >= 1; d 64, 128 or 256; page, num_blocks as above.
+ * Per token, head and group of 64: z = the largest bfloat16 <= min, s = the smallest bfloat16 >=
+ * (max - z) / 15, u = rint((x - z) / s) held to 0 .. 15 (u = 0 where s = 0), all in IEEE float32.  A group
+ * with a value, or with a range, that is not finite is held as NaN.  A slot outside the cache is skipped and
+ * reported by attn_device_status() as ATTN_ERR_INVALID_ARG.
+ */
+int attn_kv4_append(const void* k, const void* v, void* cache, const int* slots, const signed char* signs, int T,
+                    int Hk, int d, int page, int num_blocks, const long long* strides, void* stream);
+
+/*
+ * attn_kv4_read -- the values that the cache holds at T slots (a transformed K comes back transformed).
+ *
+ *   k, v        [T, Hk, d] of out_dtype (ATTN_BF16 or ATTN_FP32), contiguous, written: u * s + z rounded
+ *               once to float32 (then to bf16).  Slot -1: zeros.  A slot outside the cache: zeros, reported by
+ *               attn_device_status() as ATTN_ERR_INVALID_ARG.
+ * Slots may repeat.  Other arguments as for attn_kv4_append.
+ */
+int attn_kv4_read(const void* cache, const int* slots, void* k, void* v, int T, int Hk, int d, int page,
+                  int num_blocks, int out_dtype, void* stream);
+
+/*
+ * attn_fwd_kv4_workspace_bytes -- bytes of the workspace attn_fwd_kv4 needs (it depends on d and on the device's
+ * processor count through num_sms, not on the lengths).  num_sms 0: of the current device.  0 for a d other
+ * than 64, 128 or 256, or where there is no device to ask.
+ */
+unsigned long long attn_fwd_kv4_workspace_bytes(int d, int num_sms);
+
+/*
+ * attn_fwd_kv4 -- attention of a packed batch of queries over the 4-bit cache, with grouped heads:
+ * O = softmax(scale * Q K^T) V per request and query head, query head h reading key/value head
+ * h / (Hq / Hk), K and V the values u * s + z of the cache.
+ *
+ *   q, o        [total_q, Hq, d] bf16, device; strides: HOST pointer to 4 int64 values {row, head} of q, then
+ *               o, in elements, positive multiples of 8 (the head stride of Hq = 1 is ignored).
+ *   lse         [Hq, total_q] float32 or NULL, written: natural-log logsumexp of the scaled scores.
+ *   cache, block_table, page, num_blocks, width   as above; block_table [B, width] int32.
+ *   seq_lens    [B] int32: keys of request b, its new tokens among them; 0 .. width * page.
+ *   cu_seqlens_q  [B + 1] int32 offsets of the requests' query rows, or NULL: one query per request
+ *               (total_q = B).  Rows of q and o behind cu_seqlens_q[B] are not touched.
+ *   max_seqlen_q  >= every query length (1 without cu_seqlens_q).
+ *   signs       as given to attn_kv4_append: Q is transformed alike.  NULL: none.
+ *   causal      1: key j is visible to query i of a request iff j <= i + seq_len - query_len (the new
+ *               tokens are the last ones); 0: every key.  A row with no key gets O = 0, LSE = -inf.
+ *   workspace   attn_fwd_kv4_workspace_bytes(d, 0) bytes, 16-byte aligned, overwritten; not shared by calls
+ *               that may run at the same time.
+ * Arithmetic: scores from exact products of the codes with Q in float16 (each row scaled by a power of two so
+ * that its largest entry keeps all its bits; without the transform bf16 entries are exact over 2^-24 of it),
+ * summed in float32; softmax in float32; P times the step of V rounded to float16, summed in float32.
+ * Work is split over keys by a rule on the lengths, and the parts are joined in a fixed order: results do
+ * not depend on scheduling.  Offsets or lengths that break their rules skip that request (its rows are not
+ * written), and a table entry outside the cache leaves its keys out; both are reported by
+ * attn_device_status() as ATTN_ERR_INVALID_ARG.  What lies in a page behind a request's last key has no effect.
+ */
+int attn_fwd_kv4(const void* q, const void* cache, const int* block_table, const int* seq_lens,
+                 const int* cu_seqlens_q, void* o, float* lse, void* workspace, const signed char* signs, int B,
+                 int Hq, int Hk, int total_q, int max_seqlen_q, int d, int page, int num_blocks, int width,
+                 const long long* strides, float scale, int causal, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EXACT_ATTENTION_100_B200_ATTN_KV_H */

@@ -27,6 +27,8 @@ Modules
                       E4M3 (OCP E4M3FN) rounding/encoding, per-block quantisation.
 ``oracle.rope``       rotary position embedding (rotate-half pairing, caller's cos/sin
                       tables) in float32, ahead of the Hadamard/E4M3 pre-processing.
+``oracle.kv4``        block tables and slots request by request, the rotary embedding over several
+                      position axes, the 4-bit cache format and attention over it.
 ``oracle.attention_bwd``  the backward pass (dQ, dK, dV) from the chain rule on whole score
                       matrices, the same evaluated a block of query rows at a time (for long
                       sequences), also per sequence of a packed batch; the pages only state that
@@ -64,5 +66,10 @@ from .fp8 import (  # noqa: F401
     e4m3_decode,
     hadamard_quant_ref,
     dequant_ref,
+)
+from .kv4 import (  # noqa: F401
+    attention_kv4_ref,
+    rope_axes_ref,
+    tables_ref,
 )
 from .rope import rope_ref  # noqa: F401
