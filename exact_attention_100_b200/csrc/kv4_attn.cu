@@ -15,20 +15,27 @@
 // multiplies exactly: no conversion, 5 logic operations per 8 codes; the factors 16 are taken out of q, and of
 // O's rows at the end.  Pairs of V run over two tokens: two byte permutes bring their words together.
 //
-// One warp works on one tile of 16 keys at a time and keeps its own running maximum, sum and O.  Its tiles
-// come through its own ring of shared-memory stages, each filled by one bulk copy (a tile with all its
-// scales is contiguous) and watched by one mbarrier: no warp waits for another inside a request's keys.
-// The maximum is lazy: it moves only when a score passes it by 2^8, found by one vote per tile.  p s is
+// One warp works on two tiles of 16 keys at a time and keeps its own running maximum, sum and O.  They
+// come through its own ring of shared-memory stages, filled by one bulk copy per tile (a tile with all its
+// scales is contiguous), each stage watched by one mbarrier: no warp waits for another inside a request's
+// keys.  The maximum is lazy: it moves only when a score passes it by 2^8, found by one vote per 32 keys.  p s is
 // rounded to float16 (11 bits) under a running power-of-two reference of s, moved the same way, so that
-// values of V of any size keep their bits.
+// values of V of any size keep their bits.  The tensor core cuts its sums off (it does not round them), and codes
+// are positive, so long sums would drift; every 512 keys the middle of the codes, 7.5 times the sum of p s, moves
+// from the sums to the minima's part, which is small then too (0.5% of O over 10240 keys otherwise).
 //
-// Work is the requests' tiles laid end to end, (request, kv head, chunk of rows) after another, cut into
-// equal spans, one per block of threads.  A block that holds all tiles of a row chunk writes O; others
-// leave partial (O, m, l) in the workspace, at most two per block (its first and its last row chunk),
-// and the join kernel adds them in order.
+// Work is the requests' 32-key units laid end to end, (request, kv head, chunk of rows) after another, each
+// chunk with the cost of its prologue and epilogue in front, cut into equal spans, one per warp.  Warps
+// meet only twice, to find their spans and after their last unit.  (With a block's eight warps sharing every
+// chunk, a chunk of one unit cost the block 6 us in barriers and in latencies that nothing covered.)  A warp
+// that holds all of a chunk writes O; others leave (O, m, l) for the units they have.  A block then joins the
+// parts of its warps, which follow one another, and leaves at most two parts itself, of a chunk that began
+// before it and of one that goes on after it; the join kernel adds those, in order.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "attn_kernels.h"
 #include "kv4_format.cuh"
@@ -43,9 +50,15 @@ constexpr float kTau = 8.f;        // lazy maximum: p <= 2^kTau
 constexpr float kNegBig = -1e30f;  // below any score, and finite
 constexpr float kLn2f = 0.6931471805599453f;
 
-// A block of threads gets at least this many tiles, two for each of its warps: fewer spans than
-// blocks for short contexts, so that less is left to join
-constexpr int kMinTiles = 16;
+// Keys of a unit: two tiles, which share one wait, one vote and one round of copies (a tile at a time
+// took 421 instructions per tile, a quarter of them for those)
+constexpr int kKeys = 32;
+// What a chunk costs besides its units (its Q, its O), in units
+constexpr int kChunkCost = 3;
+// A warp gets at least this much work: fewer spans than warps for short contexts, so that less is left to join
+constexpr int kMinCost = 2;
+// Units after which the sums of codes are centred
+constexpr int kCentre = 16;
 
 template <int D, int NT>
 struct SplitCfg {
@@ -54,38 +67,44 @@ struct SplitCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlocksPerSm = D * NT <= 128 ? 2 : 1;
   static constexpr int kTile = Kv4Tile<D>::kBytes;
-  // ring of a warp: about 9 KB, 4 tiles of d = 128 (150 KB in flight per SM; 45 KB cover the latency)
-  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 3;
-  static constexpr int kRingOff = 0;
-  static constexpr int kQOff = kRingOff + kWarps * kStages * kTile;  // [kRows][D] float
-  static constexpr int kRedRow = D + 1;
-  static constexpr int kRedOff = kQOff + kRows * D * 4;              // [kWarps][kRows][D + 1] float
-  static constexpr int kMlOff = kRedOff + kWarps * kRows * kRedRow * 4;  // m, l: [2][kWarps][kRows]
-  static constexpr int kRowFOff = kMlOff + 2 * kWarps * kRows * 4;       // [kRows] score factor
-  static constexpr int kBarOff = (kRowFOff + kRows * 4 + 15) / 16 * 16;
-  static constexpr int kScanOff = kBarOff + kWarps * kStages * 8;
-  static constexpr int kSmem = kScanOff + 1024 * 8 / 4 + 64;
-  static_assert(kSmem * kBlocksPerSm + 1024 * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
+  // ring of a warp: 9 KB, 2 units of d = 128, where 16 warps share an SM (74 to 150 KB in flight; 45 KB cover
+  // the latency), twice that where 8 do
+  static constexpr int kStages = (D == 64 ? 4 : D == 128 ? 2 : 1) * (kBlocksPerSm == 1 ? 2 : 1);
+  static constexpr int kStageBytes = 2 * kTile;
+  static constexpr int kLoBytes = NT * (D / 64) * 1024;  // low parts of Q: [NT][D / 64][2][32] uint4
+  static constexpr int kWarpBytes = kStages * kStageBytes + kLoBytes;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static_assert((kSmem + 3072) * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
 };
 
-// Partial results in the workspace: per block of threads two slots of [kRows][D] float O, [kRows] m,
-// [kRows] l, then int meta: {tail valid, request, kv head, chunk, head continues}.
+// A part of a chunk: [kRows][D] float O, [kRows] m, [kRows] l.  The workspace holds per block of threads a Meta
+// and two parts (of the chunk that began before it, then of the one that goes on after it), then two parts
+// per warp, likewise.
 template <int D, int NT>
-__host__ __device__ constexpr int slot_floats() { return 8 * NT * (D + 2); }
+__host__ __device__ constexpr int part_floats() { return 8 * NT * (D + 2); }
 
 struct Meta {
-  int tail_valid;  // the block's last row chunk starts in it and goes on in the next block
+  int tail_valid;  // the last chunk starts here and goes on behind
   int b, h, chunk;
-  int head_valid;  // the block's first row chunk started before it
-  int head_ends;   // ... and ends in it
-  int pad[2];
+  int head_valid;  // the first chunk started before
+  int head_ends;   // ... and ends here
+  int rows[2];     // of the tail, of the head (a warp's)
 };
 
-// A row chunk of one request and key/value head.
-struct Item {
+// A part of a row chunk of one request and key/value head: its units [t0, t1) of `units`.
+struct Segment {
   int b, h, chunk;
   int nq, nk, q0;
-  int tiles;
+  int units, t0, t1;
+};
+
+// Where a walk over a span's segments stands.
+struct Walk {
+  long long pos;    // next position of the span
+  long long end;
+  long long first;  // position of request b's first chunk
+  long long cost;   // of request b, -1: not looked up yet
+  int b;
 };
 
 struct SeqLen {
@@ -112,20 +131,68 @@ __device__ __forceinline__ SeqLen seq_len(const Kv4AttnParams& p, int b) {
   return s;
 }
 
-// Tiles of one row chunk of a request (one, with every key masked, where it has no key).
-__device__ __forceinline__ int chunk_tiles(int nk) { return nk > 0 ? (nk + 15) >> 4 : 1; }
+// Units of one row chunk of a request (one, with every key masked, where it has no key).
+__device__ __forceinline__ int chunk_units(int nk) { return nk > 0 ? (nk + kKeys - 1) / kKeys : 1; }
 
 template <int ROWS>
-__device__ __forceinline__ long long seq_tiles(const Kv4AttnParams& p, const SeqLen& s) {
+__device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const SeqLen& s) {
   const long long chunks = (static_cast<long long>(s.nq) * p.G + ROWS - 1) / ROWS;
-  return chunks * p.Hk * chunk_tiles(s.nk);
+  return chunks * p.Hk * (chunk_units(s.nk) + kChunkCost);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// The next segment of a walk (one lane): false when the span has ended.  A boundary inside the cost in front
+// of a chunk counts as the chunk's start.
+template <int ROWS>
+__device__ __forceinline__ bool next_segment(const Kv4AttnParams& p, volatile Walk& w, volatile Segment& seg) {
+  long long pos = w.pos, first = w.first, cost = w.cost;
+  const long long end = w.end;
+  int b = w.b;
+  SeqLen s = seq_len(p, b);
+  if (cost < 0) cost = seq_cost<ROWS>(p, s);
+  while (pos < end) {
+    while (pos >= first + cost) {
+      first += cost;
+      s = seq_len(p, ++b);
+      cost = seq_cost<ROWS>(p, s);
+    }
+    const int units = chunk_units(s.nk), each = units + kChunkCost;
+    const int chunks = static_cast<int>((static_cast<long long>(s.nq) * p.G + ROWS - 1) / ROWS);
+    const long long rel = pos - first, idx = rel / each, start = first + idx * each;
+    const long long stop = min(end, start + each);
+    const int t0 = max(0, static_cast<int>(pos - start) - kChunkCost);
+    const int t1 = max(0, static_cast<int>(stop - start) - kChunkCost);
+    pos = stop;
+    if (t1 > t0) {
+      const int h = static_cast<int>(idx / chunks);
+      seg.b = b, seg.h = h, seg.chunk = static_cast<int>(idx - static_cast<long long>(h) * chunks);
+      seg.nq = s.nq, seg.nk = s.nk, seg.q0 = s.q0;
+      seg.units = units, seg.t0 = t0, seg.t1 = t1;
+      w.pos = pos, w.first = first, w.cost = cost, w.b = b;
+      return true;
+    }
+  }
+  w.pos = pos, w.first = first, w.cost = cost, w.b = b;
+  return false;
+}
+
+// d = a b + c, the warp's m16n8k16
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// The codes of the low (high) byte of each half of w as float16 subnormals, code times 2^-24: n, the even
+// one, and b, even + 16 odd.
+__device__ __forceinline__ void low_codes(uint32_t w, uint32_t& n, uint32_t& b) {
+  n = w & 0x000F000Fu;
+  b = w & 0x00FF00FFu;
+}
+__device__ __forceinline__ void high_codes(uint32_t w, uint32_t& n, uint32_t& b) {
+  b = __byte_perm(w, 0, 0x4341);
+  n = b & 0x000F000Fu;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -152,6 +219,18 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
+// Writes dimensions x, x + 1 of O (a0, a1 over sum) of a request's row, and with x = 0 its LSE.
+template <int D>
+__device__ __forceinline__ void write_row_pair(const Kv4AttnParams& p, int q0, int h, int row, int x, float a0, float a1,
+                                               float top, float sum) {
+  const int i = row / p.G, hq = h * p.G + row - i * p.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (q0 + i) * p.o_sn + hq * p.o_sh + x) =
+      pack_bf16x2(a0 * inv, a1 * inv);
+  if (x == 0 && p.lse != nullptr)
+    p.lse[static_cast<long long>(hq) * p.total_q + q0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
+}
+
 // Key of the tile that sits at index a of the products' key side: an order in which the rows that a
 // quarter (K) or half (V) warp reads together fall into different banks.
 __device__ __forceinline__ int key_at(int a) { return a ^ (((a >> 1) ^ (a >> 2)) & 1); }
@@ -163,284 +242,263 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   using F = Kv4Tile<D>;
   constexpr int GR = D / 64;  // scale groups of a row
   constexpr int ROWS = C::kRows;
+  constexpr int kQueue = C::kStages + 2;  // segments from the one being loaded back to the one being summed
   extern __shared__ __align__(128) uint8_t smem[];
-  float* sq = reinterpret_cast<float*>(smem + C::kQOff);
-  float* red = reinterpret_cast<float*>(smem + C::kRedOff);
-  float* sm_m = reinterpret_cast<float*>(smem + C::kMlOff);
-  float* sm_l = sm_m + C::kWarps * ROWS;
-  float* rowf = reinterpret_cast<float*>(smem + C::kRowFOff);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  long long* scan = reinterpret_cast<long long*>(smem + C::kScanOff);
+  __shared__ uint64_t bars[C::kWarps][C::kStages];
+  __shared__ long long scan[C::kWarps];
   __shared__ int abort_flag;
-  __shared__ long long s_first;  // tiles of the requests before s_b
-  __shared__ int s_b;
+  __shared__ Walk walks[C::kWarps];
+  __shared__ Segment queues[C::kWarps][kQueue];
+  __shared__ Meta metas[C::kWarps];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + C::kRingOff + warp * C::kStages * C::kTile;
-  uint64_t* bar = bars + warp * C::kStages;
+  uint8_t* ring = smem + warp * C::kWarpBytes;
+  uint4* slo = reinterpret_cast<uint4*>(ring + C::kStages * C::kStageBytes);
+  uint64_t* bar = bars[warp];
 
-  if (tid < C::kWarps * C::kStages) bar_init(&bars[tid], 1);
-  if (tid == 0) {
-    abort_flag = 0;
-    s_b = p.B;
-    s_first = 0;
-  }
+  if (tid < C::kWarps * C::kStages) bar_init(&bars[0][tid], 1);
+  if (tid == 0) abort_flag = 0;
   fence_barrier_init();
 
-  // ---- this block's span of the tiles: sums over the requests, a run of them per thread ----------
+  // ---- the warps' spans: sums over the requests, a run of them per thread -----------------------------
   const int per = (p.B + C::kThreads - 1) / C::kThreads;
-  const int my0 = tid * per, my1 = min(p.B, my0 + per);
+  const int my0 = min(p.B, tid * per), my1 = min(p.B, my0 + per);
   long long mine = 0;
   bool bad = false;
   for (int b = my0; b < my1; ++b) {
     const SeqLen s = seq_len(p, b);
     bad |= s.bad;
-    mine += seq_tiles<ROWS>(p, s);
+    mine += seq_cost<ROWS>(p, s);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.status, kDevStatusBadSeqlens);
-  long long incl = mine;
+  long long before = mine;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, s);
-    if (lane >= s) incl += o;
+    const long long o = __shfl_up_sync(0xffffffffu, before, s);
+    if (lane >= s) before += o;
   }
-  if (lane == 31) scan[warp] = incl;
+  if (lane == 31) scan[warp] = before;
+  before -= mine;
   __syncthreads();
-  long long total = 0, before = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < C::kWarps; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const long long blocks = min(static_cast<long long>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
+  // blocks of threads in use, all their warps alike
+  const long long blocks = min(static_cast<long long>(gridDim.x), (total + C::kWarps * kMinCost - 1) / (C::kWarps * kMinCost));
   Meta* meta = reinterpret_cast<Meta*>(p.ws) + blockIdx.x;
-  float* slots = reinterpret_cast<float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta)) +
-                 static_cast<size_t>(blockIdx.x) * 2 * slot_floats<D, NT>();
   if (blockIdx.x >= blocks) {
     if (tid == 0) *meta = Meta{};
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     return;
   }
-  const long long span0 = total * blockIdx.x / blocks, span1 = total * (blockIdx.x + 1) / blocks;
-  before += incl - mine;
-  if (before <= span0 && span0 < before + mine) {  // one thread: the span starts in its run
-    int b = my0;
-    for (;; ++b) {
-      const long long n = seq_tiles<ROWS>(p, seq_len(p, b));
-      if (span0 < before + n) break;
-      before += n;
+  const long long spans = blocks * C::kWarps;
+  for (int w = 0; w < C::kWarps; ++w) {
+    const long long i = static_cast<long long>(blockIdx.x) * C::kWarps + w;
+    const long long start = total * i / spans;
+    if (before <= start && start < before + mine) {  // one thread: the span starts in its run
+      int b = my0;
+      long long at = before;
+      for (;; ++b) {
+        const long long n = seq_cost<ROWS>(p, seq_len(p, b));
+        if (start < at + n) break;
+        at += n;
+      }
+      walks[w] = Walk{start, total * (i + 1) / spans, at, -1, b};
     }
-    s_b = b;
-    s_first = before;
   }
   __syncthreads();
 
   const AbortState ab{&abort_flag, p.status};
+  float* block_parts = reinterpret_cast<float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
+  float* warp_parts = block_parts + static_cast<size_t>(gridDim.x) * 2 * part_floats<D, NT>() +
+                      (static_cast<size_t>(blockIdx.x) * C::kWarps + warp) * 2 * part_floats<D, NT>();
+  block_parts += static_cast<size_t>(blockIdx.x) * 2 * part_floats<D, NT>();
 
-  // the row chunk and tile at a position of the span: a cursor that only moves forward
-  struct Cursor {
-    long long first;  // position of the request's first tile
-    int b;
-    SeqLen s;
-    long long n;      // tiles of the request
-  };
-  auto settle = [&](Cursor& cu, long long pos) {  // the request that holds pos (pos < total)
-    while (pos >= cu.first + cu.n) {
-      cu.first += cu.n;
-      ++cu.b;
-      cu.s = seq_len(p, cu.b);
-      cu.n = seq_tiles<ROWS>(p, cu.s);
-    }
-  };
-  auto item_at = [&](const Cursor& cu, long long pos, Item& it) -> int {  // returns the tile in the chunk
-    it.b = cu.b;
-    it.nq = cu.s.nq;
-    it.nk = cu.s.nk;
-    it.q0 = cu.s.q0;
-    it.tiles = chunk_tiles(cu.s.nk);
-    const long long rel = pos - cu.first;
-    const long long idx = rel / it.tiles;
-    const int chunks = (it.nq * p.G + ROWS - 1) / ROWS;
-    it.h = static_cast<int>(idx / chunks);
-    it.chunk = static_cast<int>(idx - static_cast<long long>(it.h) * chunks);
-    return static_cast<int>(rel - idx * it.tiles);
-  };
-
-  // ---- producer side: the warp's tiles of the span, in order; lane 0 issues the copies ------------------
-  Cursor pc{s_first, s_b, seq_len(p, s_b), 0};
-  pc.n = seq_tiles<ROWS>(p, pc.s);
-  long long ppos = span0;    // start of the row chunk (or its part) being loaded
-  int p_end = 0;             // tiles [.., p_end) of it are in the span
-  int p_next = 0;            // next tile of this warp
-  int p_blk_base = 0;        // tile that lane 0's table entry belongs to
-  int p_blk = -1;            // lane i: block of tile p_blk_base + kWarps * i
-  Item pit{};
+  // ---- producer side: the units of the span, in order; segments go into the warp's queue --------------
+  int p_seg = -1;            // segments opened, less one
+  int p_end = 0;             // units [.., p_end) of it are in the span
+  int p_next = 0;            // next unit
+  int p_base = 0;            // lane i keeps the address of tile i & 1 of unit p_base + i / 2 of the chunk, or
+  const uint8_t* p_addr = nullptr;  // nullptr: past the keys, or no block of the cache
   bool p_more = true;
-  uint32_t bad_stage = 0;    // stages whose tile was not loaded
-  auto table_window = [&]() {
-    p_blk_base = p_next;
-    const int t = p_next + C::kWarps * lane;
-    p_blk = -1;
-    if (t < p_end && t * 16 < pit.nk) {
-      const int e = __ldg(p.table + static_cast<long long>(pit.b) * p.width + (t * 16) / p.page);
-      if (e >= 0 && e < p.num_blocks) p_blk = e;
-      else atomicOr(p.status, kDevStatusBadSeqlens);
-    }
-  };
-  auto open_chunk = [&]() {  // moves to the row chunk at ppos; p_more: there is one
-    p_more = ppos < span1;
-    if (!p_more) return;
-    settle(pc, ppos);
-    const int t0 = item_at(pc, ppos, pit);
-    const long long left = span1 - ppos;
-    p_end = left < pit.tiles - t0 ? t0 + static_cast<int>(left) : pit.tiles;
-    ppos += p_end - t0;
-    p_next = t0 + warp;
-    table_window();
-  };
-  int p_stage = 0;
+  uint32_t absent = 0;       // 2 bits per stage: its tiles that were not loaded
   int in_flight = 0;
-  auto produce = [&]() {  // fills the next stage, if the warp has a tile left
-    while (p_more && p_next >= p_end) open_chunk();
-    if (!p_more) return;
-    if (p_next - p_blk_base >= 32 * C::kWarps) table_window();
-    const int blk = __shfl_sync(0xffffffffu, p_blk, (p_next - p_blk_base) / C::kWarps);
-    const int off = (p_next * 16) % p.page;
-    if (blk >= 0) {
-      bad_stage &= ~(1u << p_stage);
-      if (lane == 0) {
-        bar_arrive_expect_tx(&bar[p_stage], C::kTile);
-        bulk_load_g2s(ring + p_stage * C::kTile, p.cache + kv4_tile_offset<D>(blk, off, p.page, p.Hk, pit.h),
-                      C::kTile, &bar[p_stage]);
+  auto produce = [&](int at) {  // fills stage `at`, if there is a unit left
+    if (p_more && p_next >= p_end) {
+      volatile Segment& seg = queues[warp][(p_seg + 1) % kQueue];
+      int more = 0;
+      if (lane == 0) more = next_segment<ROWS>(p, walks[warp], seg);
+      p_more = __shfl_sync(0xffffffffu, more, 0) != 0;
+      __syncwarp();
+      if (p_more) {
+        ++p_seg;
+        p_next = seg.t0;
+        p_end = seg.t1;
+        p_base = p_next - 16;  // no window yet
       }
-    } else {
-      bad_stage |= 1u << p_stage;
-      if (lane == 0) bar_arrive(&bar[p_stage]);
     }
+    if (!p_more) return;
+    if (p_next - p_base >= 16) {
+      volatile Segment& seg = queues[warp][p_seg % kQueue];
+      p_base = p_next;
+      const int u = p_next + (lane >> 1);
+      const int key = u * kKeys + 16 * (lane & 1);
+      p_addr = nullptr;
+      if (u < p_end && key < seg.nk) {
+        const int j = key / p.page;
+        const int e = __ldg(p.table + static_cast<long long>(seg.b) * p.width + j);
+        if (e >= 0 && e < p.num_blocks)
+          p_addr = p.cache + kv4_tile_offset<D>(e, key - j * p.page, p.page, p.Hk, seg.h);
+        else
+          atomicOr(p.status, kDevStatusBadSeqlens);
+      }
+      __syncwarp();
+    }
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(
+        0xffffffffu, reinterpret_cast<unsigned long long>(p_addr), 2 * (p_next - p_base) + (lane & 1)));
+    const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr) & 3u;
+    absent = (absent & ~(3u << (2 * at))) | ((have ^ 3u) << (2 * at));
+    if (lane == 0) bar_arrive_expect_tx(&bar[at], __popc(have) * C::kTile);
+    __syncwarp();
+    if (lane < 2 && src != nullptr)
+      bulk_load_g2s(ring + at * C::kStageBytes + lane * C::kTile, src, C::kTile, &bar[at]);
     ++in_flight;
-    p_next += C::kWarps;
-    p_stage = p_stage + 1 == C::kStages ? 0 : p_stage + 1;
+    ++p_next;
   };
-  open_chunk();
 #pragma unroll 1
-  for (int i = 0; i < C::kStages; ++i) produce();
+  for (int i = 0; i < C::kStages; ++i) produce(i);
 
   // ---- consumer side --------------------------------------------------------------------------------------
-  Cursor cc{s_first, s_b, seq_len(p, s_b), 0};
-  cc.n = seq_tiles<ROWS>(p, cc.s);
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;  // false once a wait ran out: no more copies, and those in flight are waited for
-  bool tail_valid = false, head_valid = false, head_ends = false;
-  Item it{};
+  if (lane == 0) metas[warp] = Meta{};
 #pragma unroll 1
-  for (long long pos = span0; pos < span1;) {
-    settle(cc, pos);
-    const int t0 = item_at(cc, pos, it);
-    const long long left = span1 - pos;
-    const int t1 = left < it.tiles - t0 ? t0 + static_cast<int>(left) : it.tiles;
-    pos += t1 - t0;
-    const int rows = min(ROWS, it.nq * p.G - it.chunk * ROWS);
+  for (int seg_no = 0; seg_no <= p_seg; ++seg_no) {
+    volatile Segment& it = queues[warp][seg_no % kQueue];
+    const int t0 = it.t0, t1 = it.t1;
     const int row0 = it.chunk * ROWS;
+    const int rows = min(ROWS, it.nq * p.G - row0);
 
-    // Q of the chunk: one warp per row, transformed in float32, scaled by a power of two
-    for (int r = warp; r < ROWS; r += C::kWarps) {
-      constexpr int E = D / 32;  // consecutive elements of a lane
-      float x[E];
+    // Q, as the operand of row n = g (one of 8 per NT): this lane has entries 16 c .. 16 c + 15 of every group.
+    // Transformed in float32 (strides 16 and 32 lie between lanes), scaled by a power of two that puts the row's
+    // largest entry at 2^13 .. 2^14 (cf takes it back, and the 2^-24 of the codes).
+    // A byte of codes is b = even + 16 odd, so with cb = q_odd / 16 and cn = q_even - cb the products
+    // cn even + cb b are q_even even + q_odd odd.  Both are kept as two float16, the rounded value and what its
+    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).  qs: sums of a
+    // group's entries, times 2^-24.
+    uint32_t qf[NT][GR][4][2];
+    float qs[NT][GR][2];  // rows 2c, 2c + 1
+    float cf[NT][2];
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
-      if (r < rows) {
-        const int i = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - i * p.G;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (it.q0 + i) * p.q_sn + hq * p.q_sh + E * lane;
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[GR][16];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
-          x[e] = __uint_as_float(w << 16);
-          x[e + 1] = __uint_as_float(w & 0xFFFF0000u);
+      for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[gr][i] = 0.f;
+      if (8 * nt + g < rows) {
+        const int r = row0 + 8 * nt + g, i = r / p.G, hq = it.h * p.G + r - i * p.G;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (it.q0 + i) * p.q_sn + hq * p.q_sh + 16 * c;
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + 64 * gr), v = *reinterpret_cast<const uint4*>(src + 64 * gr + 8);
+          const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[gr][2 * j] = __uint_as_float(w[j] << 16);
+            x[gr][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          }
         }
       }
       if (p.signs != nullptr) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (p.signs[E * lane + e] == -1) x[e] = -x[e];
+        for (int gr = 0; gr < GR; ++gr) {
+          const int4 sg = *reinterpret_cast<const int4*>(p.signs + 64 * gr + 16 * c);
+          const int sw[4] = {sg.x, sg.y, sg.z, sg.w};
 #pragma unroll
-        for (int s = 1; s < E; s <<= 1)
+          for (int i = 0; i < 16; ++i)
+            if (static_cast<signed char>(sw[i >> 2] >> (8 * (i & 3))) == -1) x[gr][i] = -x[gr][i];
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (!(e & s)) {
-              const float u = x[e], v = x[e | s];
-              x[e] = u + v;
-              x[e | s] = u - v;
+          for (int st = 1; st < 16; st <<= 1)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!(i & st)) {
+                const float a = x[gr][i], b = x[gr][i | st];
+                x[gr][i] = a + b;
+                x[gr][i | st] = a - b;
+              }
+#pragma unroll
+          for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float o2 = __shfl_xor_sync(0xffffffffu, x[gr][i], st);
+              x[gr][i] = (c & st) ? o2 - x[gr][i] : x[gr][i] + o2;
             }
+        }
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1)
+        for (int st = 1; st < GR; st <<= 1)
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float o = __shfl_xor_sync(0xffffffffu, x[e], s);
-            x[e] = (lane & s) ? o - x[e] : x[e] + o;
-          }
+          for (int gr = 0; gr < GR; ++gr)
+            if (!(gr & st))
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float a = x[gr][i], b = x[gr | st][i];
+                x[gr][i] = a + b;
+                x[gr | st][i] = a - b;
+              }
       }
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
+      for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-      for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      // the largest entry at 2^13 .. 2^14; the factor of the scores takes it back, and the 2^-24
-      // of the codes
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[gr][i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = top > 0.f ? min(max(exponent_of(top) - 13, -100), 100) : 0;
-      const float f = exp2_int(-ex);
-#pragma unroll
-      for (int e = 0; e < E; ++e) sq[r * D + E * lane + e] = x[e] * f;
-      if (lane == 0) rowf[r] = p.scale_log2 * exp2_int(ex) * 16777216.f;
-    }
-    __syncthreads();
-
-    // operand of row n = g (one of 8 per NT): b0 pairs (r, r + 4), b1 pairs (r + 1, r + 5) / 16 of
-    // 16 c + (0 | 2 | 8 | 10) in each group, and sums of the rounded entries per group
-    uint32_t qf[NT][GR][4][2];
-    float qs[NT][GR][2];  // rows 2c, 2c + 1
-    float cf[NT][2];
-    int lim[NT][2];       // keys that rows 2c, 2c + 1 see
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      const float f = exp2_int(-ex), back = p.scale_log2 * exp2_int(ex) * 16777216.f;
+      cf[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+      cf[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
-        float q16[16], sum = 0.f;
-        const float4* src = reinterpret_cast<const float4*>(sq + (8 * nt + g) * D + 64 * gr + 16 * c);
+        float hn[8], hb[8], ln[8], lb[8], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = src[i];
-          q16[4 * i] = v.x, q16[4 * i + 1] = v.y, q16[4 * i + 2] = v.z, q16[4 * i + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float h = __half2float(__float2half_rn((i & 1) ? q16[i] * 0.0625f : q16[i]));
-          q16[i] = h;
-          sum += (i & 1) ? h * 16.f : h;
+        for (int k = 0; k < 8; ++k) {
+          const float cb = x[gr][2 * k + 1] * f * 0.0625f, cn = x[gr][2 * k] * f - cb;
+          hb[k] = __half2float(__float2half_rn(cb));
+          lb[k] = __half2float(__float2half_rn(cb - hb[k]));
+          hn[k] = __half2float(__float2half_rn(cn));
+          ln[k] = __half2float(__float2half_rn(cn - hn[k]));
+          sum += (hn[k] + ln[k]) + 17.f * (hb[k] + lb[k]);
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const int o = (ks >> 1) * 8 + (ks & 1) * 2;
-          qf[nt][gr][ks][0] = pack_f16x2(q16[o], q16[o + 4]);
-          qf[nt][gr][ks][1] = pack_f16x2(q16[o + 1], q16[o + 5]);
+          const int k = 4 * (ks >> 1) + (ks & 1);
+          qf[nt][gr][ks][0] = pack_f16x2(hn[k], hn[k + 2]);
+          qf[nt][gr][ks][1] = pack_f16x2(hb[k], hb[k + 2]);
         }
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)
+          slo[((nt * GR + gr) * 2 + k / 4) * 32 + lane] =
+              make_uint4(pack_f16x2(ln[k], ln[k + 2]), pack_f16x2(lb[k], lb[k + 2]),
+                         pack_f16x2(ln[k + 1], ln[k + 3]), pack_f16x2(lb[k + 1], lb[k + 3]));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         sum *= 1.f / 16777216.f;
         qs[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
         qs[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * c + e;
-        cf[nt][e] = rowf[r];
-        lim[nt][e] = p.causal && r < rows ? min(it.nk, max(0, it.nk - it.nq + (row0 + r) / p.G + 1)) : it.nk;
-      }
     }
+    __syncwarp();
     const int min_lim = p.causal ? min(it.nk, max(0, it.nk - it.nq + row0 / p.G + 1)) : it.nk;
 
     float m[NT][2], l[NT][2], zacc[NT][GR][2], o[NT][D / 16][4];
+    float ps[NT][GR][2];       // sums of p s 2^-E of the lane's keys since the sums of codes were centred
+    int uncentred = 0;
     float ef = exp2_int(100);  // 2^-E, E the reference exponent of V's steps
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -449,7 +507,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
         m[nt][e] = kNegBig;
         l[nt][e] = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) zacc[nt][gr][e] = 0.f;
+        for (int gr = 0; gr < GR; ++gr) zacc[nt][gr][e] = ps[nt][gr][e] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -458,7 +516,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     }
 
 #pragma unroll 1
-    for (int t = t0 + warp; t < t1; t += C::kWarps) {
+    for (int t = t0; t < t1; ++t) {
       if (alive) {
         if (!warp_all(wait_bar(&bar[stage], phase, ab))) {
           alive = p_more = false;
@@ -468,308 +526,479 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
         drain(&bar[stage], phase);
       }
       in_flight = max(in_flight - 1, 0);
-      const uint8_t* tile = ring + stage * C::kTile;
-      const int key0 = t * 16;
-      const bool missing = (bad_stage >> stage) & 1u;
-      const bool whole = !missing && key0 + 16 <= min_lim;
-      const int ka = key0 + key_at(g), kb = ka + 8;  // this lane's keys of the scores
-
-      // scores: y = sum_g s (q . u) + z (sum q)
-      float y[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[nt][e] = 0.f;
-#pragma unroll
-      for (int pl = 0; pl < F::kPlanes; ++pl) {
-        const uint8_t* ra = tile + pl * F::kPlaneBytes + key_at(g) * F::kRowBytes + c * 8 * F::kGroups;
-        uint32_t wa[2 * F::kGroups], wb[2 * F::kGroups];
-        if constexpr (F::kGroups == 2) {
-          const uint4 u = *reinterpret_cast<const uint4*>(ra);
-          const uint4 v = *reinterpret_cast<const uint4*>(ra + 8 * F::kRowBytes);
-          wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w;
-          wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(ra);
-          const uint2 v = *reinterpret_cast<const uint2*>(ra + 8 * F::kRowBytes);
-          wa[0] = u.x, wa[1] = u.y;
-          wb[0] = v.x, wb[1] = v.y;
-        }
-#pragma unroll
-        for (int gp = 0; gp < F::kGroups; ++gp) {
-          const int gr = pl * F::kGroups + gp;
-          float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t a = wa[2 * gp + (ks >> 1)] >> (8 * (ks & 1));
-            const uint32_t b = wb[2 * gp + (ks >> 1)] >> (8 * (ks & 1));
-            const uint32_t fr[4] = {a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt], fr, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
-          }
-          const uint32_t za = *reinterpret_cast<const uint32_t*>(tile + F::kKszOff + key_at(g) * F::kSzRow + 4 * gr);
-          const uint32_t zb = *reinterpret_cast<const uint32_t*>(tile + F::kKszOff + (key_at(g) + 8) * F::kSzRow + 4 * gr);
-          const float s0 = __uint_as_float(za << 16), z0 = __uint_as_float(za & 0xFFFF0000u);
-          const float s1 = __uint_as_float(zb << 16), z1 = __uint_as_float(zb & 0xFFFF0000u);
+      const int key0 = t * kKeys;
+      const uint32_t gone = (absent >> (2 * stage)) & 3u;
+      auto step = [&](auto whole_unit) {
+        constexpr bool whole = decltype(whole_unit)::value;
+        // masks: whether this lane's key e (of two) of tile ti is one of the request's, and the number of keys
+        // that row 2c + e2 of set nt sees
+        const int ka = key0 + key_at(g);
+        int nk = 0;
+        if constexpr (!whole) nk = it.nk;
+        auto held = [&](int ti, int e) { return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < nk; };
+        int lim[NT][2];
+        if constexpr (!whole) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              y[nt][e] = fmaf(z0, qs[nt][gr][e], fmaf(s0, acc[nt][e], y[nt][e]));
-              y[nt][2 + e] = fmaf(z1, qs[nt][gr][e], fmaf(s1, acc[nt][2 + e], y[nt][2 + e]));
+              const int r = 8 * nt + 2 * c + e;
+              lim[nt][e] = p.causal && r < rows ? min(nk, nk - it.nq + (row0 + r) / p.G + 1) : nk;
             }
         }
-      }
-      bool over = false;
+        auto sees = [&](int ti, int e, int nt, int e2) {
+          return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < lim[nt][e2];
+        };
+
+        // scores: y = sum_g s (q . u) + z (sum q), in units of log2
+        float y[2][NT][4];
+        bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int pl = 0; pl < F::kPlanes; ++pl) {
+          uint32_t wa[2][2 * F::kGroups], wb[2][2 * F::kGroups], sza[2][F::kGroups], szb[2][F::kGroups];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = y[nt][e] * cf[nt][e & 1];
-          if (!whole && (missing || (e < 2 ? ka : kb) >= lim[nt][e & 1])) x = -INFINITY;
-          y[nt][e] = x;
-          over = over || x > m[nt][e & 1] + kTau;
+          for (int ti = 0; ti < 2; ++ti) {
+            const uint8_t* tile = ring + stage * C::kStageBytes + ti * C::kTile;
+            const uint8_t* ra = tile + pl * F::kPlaneBytes + key_at(g) * F::kRowBytes + c * 8 * F::kGroups;
+            const uint8_t* rz = tile + F::kKszOff + key_at(g) * F::kSzRow + 4 * pl * F::kGroups;
+            if constexpr (F::kGroups == 2) {
+              const uint4 u = *reinterpret_cast<const uint4*>(ra);
+              const uint4 v = *reinterpret_cast<const uint4*>(ra + 8 * F::kRowBytes);
+              wa[ti][0] = u.x, wa[ti][1] = u.y, wa[ti][2] = u.z, wa[ti][3] = u.w;
+              wb[ti][0] = v.x, wb[ti][1] = v.y, wb[ti][2] = v.z, wb[ti][3] = v.w;
+              const uint2 x = *reinterpret_cast<const uint2*>(rz);
+              const uint2 z = *reinterpret_cast<const uint2*>(rz + 8 * F::kSzRow);
+              sza[ti][0] = x.x, sza[ti][1] = x.y, szb[ti][0] = z.x, szb[ti][1] = z.y;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(ra);
+              const uint2 v = *reinterpret_cast<const uint2*>(ra + 8 * F::kRowBytes);
+              wa[ti][0] = u.x, wa[ti][1] = u.y;
+              wb[ti][0] = v.x, wb[ti][1] = v.y;
+              sza[ti][0] = *reinterpret_cast<const uint32_t*>(rz);
+              szb[ti][0] = *reinterpret_cast<const uint32_t*>(rz + 8 * F::kSzRow);
+            }
+          }
+#pragma unroll
+          for (int gp = 0; gp < F::kGroups; ++gp) {
+            const int gr = pl * F::kGroups + gp;
+            float acc[2][NT][4];
+#pragma unroll
+            for (int kp = 0; kp < 2; ++kp) {
+              uint4 lo[NT];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) lo[nt] = slo[((nt * GR + gr) * 2 + kp) * 32 + lane];
+#pragma unroll
+              for (int ti = 0; ti < 2; ++ti) {
+                uint32_t f0[4], f1[4];
+                low_codes(wa[ti][2 * gp + kp], f0[0], f0[2]);
+                low_codes(wb[ti][2 * gp + kp], f0[1], f0[3]);
+                high_codes(wa[ti][2 * gp + kp], f1[0], f1[2]);
+                high_codes(wb[ti][2 * gp + kp], f1[1], f1[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&ac)[4] = acc[ti][nt];
+                  constexpr float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                  if (kp == 0) mma16816(ac, f0, qf[nt][gr][0][0], qf[nt][gr][0][1], zero);
+                  else mma16816(ac, f0, qf[nt][gr][2][0], qf[nt][gr][2][1], ac);
+                  mma16816(ac, f0, lo[nt].x, lo[nt].y, ac);
+                  mma16816(ac, f1, qf[nt][gr][2 * kp + 1][0], qf[nt][gr][2 * kp + 1][1], ac);
+                  mma16816(ac, f1, lo[nt].z, lo[nt].w, ac);
+                }
+              }
+            }
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti) {
+              const float s0 = __uint_as_float(sza[ti][gp] << 16), z0 = __uint_as_float(sza[ti][gp] & 0xFFFF0000u);
+              const float s1 = __uint_as_float(szb[ti][gp] << 16), z1 = __uint_as_float(szb[ti][gp] & 0xFFFF0000u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float a0 = s0 * acc[ti][nt][e], a1 = s1 * acc[ti][nt][2 + e];
+                  const float b0 = gr == 0 ? a0 : fmaf(s0, acc[ti][nt][e], y[ti][nt][e]);
+                  const float b1 = gr == 0 ? a1 : fmaf(s1, acc[ti][nt][2 + e], y[ti][nt][2 + e]);
+                  y[ti][nt][e] = fmaf(z0, qs[nt][gr][e], b0);
+                  y[ti][nt][2 + e] = fmaf(z1, qs[nt][gr][e], b1);
+                }
+            }
+          }
         }
-      // V's steps and minima of the lane's keys
-      float vs[GR][2], vz[GR][2];
-      float smax = 0.f;
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
+        for (int ti = 0; ti < 2; ++ti)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + F::kVszOff + (key_at(g) + 8 * e) * F::kSzRow + 4 * gr);
-          vs[gr][e] = __uint_as_float(w << 16);
-          vz[gr][e] = __uint_as_float(w & 0xFFFF0000u);
-          if (!whole && (missing || (e ? kb : ka) >= it.nk)) vs[gr][e] = vz[gr][e] = 0.f;
-          smax = fmaxf(smax, vs[gr][e]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = y[ti][nt][e] * cf[nt][e & 1];
+              if constexpr (!whole) x = sees(ti, e >> 1, nt, e & 1) ? x : -INFINITY;
+              y[ti][nt][e] = x;
+              over = over || x > m[nt][e & 1] + kTau;
+            }
+        // V's steps and minima of the lane's keys, as they are held
+        float smax = 0.f;
+        uint32_t vw[2][2][GR];
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          const uint8_t* tile = ring + stage * C::kStageBytes + ti * C::kTile;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* rz = tile + F::kVszOff + (key_at(g) + 8 * e) * F::kSzRow;
+            if constexpr (GR == 1) {
+              vw[ti][e][0] = *reinterpret_cast<const uint32_t*>(rz);
+            } else {
+#pragma unroll
+              for (int gr = 0; gr < GR; gr += 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(rz + 4 * gr);
+                vw[ti][e][gr] = v.x, vw[ti][e][gr + 1] = v.y;
+              }
+            }
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+              if constexpr (!whole)
+                if (!held(ti, e)) vw[ti][e][gr] = 0u;
+              smax = fmaxf(smax, __uint_as_float(vw[ti][e][gr] << 16));
+            }
+          }
         }
-      over = over || smax * ef > 32.f;
-      if (__any_sync(0xffffffffu, over)) {  // rare: move the references, and what was summed under them
+        over = over || smax * ef > 32.f;
+        if (__any_sync(0xffffffffu, over)) {  // rare: move the references, and what was summed under them
 #pragma unroll
-        for (int sft = 4; sft < 32; sft <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, sft));
-        float fe = 1.f;
-        if (smax * ef > 32.f) {
-          const float nf = exp2_int(-min(exponent_of(smax), 120));
-          fe = nf / ef;
-          ef = nf;
+          for (int sft = 4; sft < 32; sft <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, sft));
+          float fe = 1.f;
+          if (smax * ef > 32.f) {
+            const float nf = exp2_int(-min(exponent_of(smax), 120));
+            fe = nf / ef;
+            ef = nf;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(fmaxf(y[0][nt][e], y[0][nt][2 + e]), fmaxf(y[1][nt][e], y[1][nt][2 + e]));
+#pragma unroll
+              for (int sft = 4; sft < 32; sft <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
+              const float nm = fmaxf(m[nt][e], top);
+              const float al = ex2_approx(m[nt][e] - nm);
+              m[nt][e] = nm;
+              l[nt][e] *= al;
+              const float oe = al * fe;
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr) {
+                zacc[nt][gr][e] *= al;
+                ps[nt][gr][e] *= oe;
+              }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[nt][i][e] *= oe;
+                o[nt][i][2 + e] *= oe;
+              }
+            }
         }
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          const uint8_t* tile = ring + stage * C::kStageBytes + ti * C::kTile;
+          // p, its sum, the minima's part, and p s as the operand of the second product
+          uint32_t pf[NT][GR][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(y[ti][nt][e] - m[nt][e & 1]);
+            l[nt][0] += pr[0] + pr[2];
+            l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+              float t4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t w = vw[ti][e >> 1][gr];
+                const float z = __uint_as_float(w & 0xFFFF0000u);
+                t4[e] = pr[e] * (__uint_as_float(w << 16) * ef);
+                if constexpr (whole) {
+                  zacc[nt][gr][e & 1] = fmaf(pr[e], z, zacc[nt][gr][e & 1]);
+                } else if (sees(ti, e >> 1, nt, e & 1)) {
+                  zacc[nt][gr][e & 1] = fmaf(pr[e], z, zacc[nt][gr][e & 1]);
+                } else {  // a masked key adds nothing, whatever its scales are (NaN among them)
+                  t4[e] = 0.f;
+                }
+              }
+              ps[nt][gr][0] += t4[0] + t4[2];
+              ps[nt][gr][1] += t4[1] + t4[3];
+              pf[nt][gr][0] = transpose8x8(pack_f16x2(t4[0], t4[1]));
+              pf[nt][gr][1] = transpose8x8(pack_f16x2(t4[2], t4[3]));
+            }
+          }
+          // O^T += u^T (p s): dimensions 8 g + 2 q (and + 1, times 16) of each group on the 16 side
+#pragma unroll
+          for (int pl = 0; pl < F::kPlanes; ++pl) {
+            const uint8_t* rv = tile + F::kVOff + pl * F::kPlaneBytes + g * 4 * F::kGroups;
+            uint32_t w[4][F::kGroups];  // tokens at indices 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint8_t* r = rv + (key_at(2 * c + (i & 1)) + 8 * (i >> 1)) * F::kRowBytes;
+              if constexpr (F::kGroups == 2) {
+                const uint2 u = *reinterpret_cast<const uint2*>(r);
+                w[i][0] = u.x, w[i][1] = u.y;
+              } else {
+                w[i][0] = *reinterpret_cast<const uint32_t*>(r);
+              }
+            }
+#pragma unroll
+            for (int gp = 0; gp < F::kGroups; ++gp) {
+              const int gr = pl * F::kGroups + gp;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t u = __byte_perm(w[0][gp], w[1][gp], hf ? 0x7632 : 0x5410);
+                const uint32_t v = __byte_perm(w[2][gp], w[3][gp], hf ? 0x7632 : 0x5410);
+                uint32_t f0[4], f1[4];  // even codes on the first 8 rows, bytes on the others
+                low_codes(u, f0[0], f0[1]);
+                low_codes(v, f0[2], f0[3]);
+                high_codes(u, f1[0], f1[1]);
+                high_codes(v, f1[2], f1[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&o0)[4] = o[nt][4 * gr + 2 * hf], (&o1)[4] = o[nt][4 * gr + 2 * hf + 1];
+                  mma16816(o0, f0, pf[nt][gr][0], pf[nt][gr][1], o0);
+                  mma16816(o1, f1, pf[nt][gr][0], pf[nt][gr][1], o1);
+                }
+              }
+            }
+          }
+        }
+      };
+      // a unit that every row sees whole needs no masks
+      if (gone == 0 && key0 + kKeys <= min_lim) step(std::true_type{});
+      else step(std::false_type{});
+      if (++uncentred == kCentre) {
+        uncentred = 0;
+        const float per_step = 7.5f / ef;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(y[nt][e], y[nt][2 + e]);
+          for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-            for (int sft = 4; sft < 32; sft <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
-            const float nm = fmaxf(m[nt][e], top);
-            const float al = ex2_approx(m[nt][e] - nm);
-            m[nt][e] = nm;
-            l[nt][e] *= al;
+            for (int e = 0; e < 2; ++e) {
+              float all = ps[nt][gr][e];
+              zacc[nt][gr][e] = fmaf(per_step, all, zacc[nt][gr][e]);
+              ps[nt][gr][e] = 0.f;
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) zacc[nt][gr][e] *= al;
-            const float oe = al * fe;
+              for (int sft = 4; sft < 32; sft <<= 1) all += __shfl_xor_sync(0xffffffffu, all, sft);
+              all *= 7.5f / 16777216.f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[nt][i][e] *= oe;
-              o[nt][i][2 + e] *= oe;
+              for (int k = 0; k < 4; ++k) {
+                o[nt][4 * gr + k][e] -= all;
+                o[nt][4 * gr + k][2 + e] -= 17.f * all;
+              }
             }
-          }
-      }
-      // p, its sum, the minima's part, and p s as the operand of the second product
-      uint32_t pf[NT][GR][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(y[nt][e] - m[nt][e & 1]);
-        l[nt][0] += pr[0] + pr[2];
-        l[nt][1] += pr[1] + pr[3];
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          float t4[4], z4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t4[e] = pr[e] * (vs[gr][e >> 1] * ef);
-            z4[e] = pr[e] * vz[gr][e >> 1];
-          }
-          if (!whole) {  // a masked key adds nothing, whatever its scales are (NaN among them)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (missing || (e < 2 ? ka : kb) >= lim[nt][e & 1]) t4[e] = z4[e] = 0.f;
-          }
-          zacc[nt][gr][0] += z4[0] + z4[2];
-          zacc[nt][gr][1] += z4[1] + z4[3];
-          pf[nt][gr][0] = transpose8x8(pack_f16x2(t4[0], t4[1]));
-          pf[nt][gr][1] = transpose8x8(pack_f16x2(t4[2], t4[3]));
-        }
-      }
-      // O^T += u^T (p s): dimensions 8 g + 2 q (and + 1, times 16) of each group on the 16 side
-#pragma unroll
-      for (int pl = 0; pl < F::kPlanes; ++pl) {
-        const uint8_t* rv = tile + F::kVOff + pl * F::kPlaneBytes + g * 4 * F::kGroups;
-        uint32_t w[4][F::kGroups];  // tokens at indices 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* r = rv + (key_at(2 * c + (i & 1)) + 8 * (i >> 1)) * F::kRowBytes;
-          if constexpr (F::kGroups == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(r);
-            w[i][0] = u.x, w[i][1] = u.y;
-          } else {
-            w[i][0] = *reinterpret_cast<const uint32_t*>(r);
-          }
-        }
-#pragma unroll
-        for (int gp = 0; gp < F::kGroups; ++gp) {
-          const int gr = pl * F::kGroups + gp;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t u = __byte_perm(w[0][gp], w[1][gp], hf ? 0x7632 : 0x5410);
-            const uint32_t v = __byte_perm(w[2][gp], w[3][gp], hf ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int q2 = 0; q2 < 2; ++q2) {
-              const uint32_t a = u >> (8 * q2), b = v >> (8 * q2);
-              const uint32_t fr[4] = {a & 0x000F000Fu, a & 0x00F000F0u, b & 0x000F000Fu, b & 0x00F000F0u};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * gr + 2 * hf + q2], fr, pf[nt][gr][0], pf[nt][gr][1]);
-            }
-          }
-        }
       }
       __syncwarp();
+      produce(stage);
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
-      produce();
     }
 
-    // ---- join the warps -------------------------------------------------------------------------------
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float s = l[nt][e];
-#pragma unroll
-        for (int sft = 4; sft < 32; sft <<= 1) s += __shfl_xor_sync(0xffffffffu, s, sft);
-        l[nt][e] = s;
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          float z = zacc[nt][gr][e];
-#pragma unroll
-          for (int sft = 4; sft < 32; sft <<= 1) z += __shfl_xor_sync(0xffffffffu, z, sft);
-          zacc[nt][gr][e] = z;
-        }
-        if (g == 0) {
-          sm_m[warp * ROWS + 8 * nt + 2 * c + e] = m[nt][e];
-          sm_l[warp * ROWS + 8 * nt + 2 * c + e] = s;
-        }
-      }
-    __syncthreads();
-    const float back = 16777216.f / ef;
+    // ---- O, or this segment's part of it: this lane has dimensions 8 g .. 8 g + 7 of every group of rows 2c, 2c + 1
+    const bool starts = it.t0 == 0, ends = it.t1 == it.units;
+    const float unscale = 16777216.f / ef;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * nt + 2 * c + e;
-        float top = kNegBig;
+        float sum = l[nt][e];
 #pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm_m[w * ROWS + r]);
-        const float f = ex2_approx(m[nt][e] - top);
-        float* dst = red + (warp * ROWS + r) * C::kRedRow;
+        for (int sft = 4; sft < 32; sft <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sft);
+        const bool whole_chunk = starts && ends;
+        const float inv = whole_chunk ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        const int i = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - i * p.G;
+        float* part = warp_parts + (starts ? part_floats<D, NT>() : 0);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int dim = 64 * (i >> 2) + 8 * g + 2 * (i & 3);
-          dst[dim] = (o[nt][i][e] * back + zacc[nt][i >> 2][e]) * f;
-          dst[dim + 1] = (o[nt][i][2 + e] * (back * 0.0625f) + zacc[nt][i >> 2][e]) * f;
+        for (int gr = 0; gr < GR; ++gr) {
+          float z = zacc[nt][gr][e];
+#pragma unroll
+          for (int sft = 4; sft < 32; sft <<= 1) z += __shfl_xor_sync(0xffffffffu, z, sft);
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float n = o[nt][4 * gr + k][e], b = o[nt][4 * gr + k][2 + e];
+            v[2 * k] = (n * unscale + z) * inv;
+            v[2 * k + 1] = ((b - n) * (unscale * 0.0625f) + z) * inv;
+          }
+          if (r < rows) {
+            if (whole_chunk) {
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (it.q0 + i) * p.o_sn + hq * p.o_sh + 64 * gr + 8 * g) =
+                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + r * D + 64 * gr + 8 * g);
+              dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+              dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+        }
+        if (g == 0 && r < rows) {
+          if (!whole_chunk) {
+            part[ROWS * D + r] = m[nt][e];
+            part[ROWS * D + ROWS + r] = sum;
+          } else if (p.lse != nullptr) {
+            p.lse[static_cast<long long>(hq) * p.total_q + it.q0 + i] =
+                sum == 0.f ? -INFINITY : (m[nt][e] + log2f(sum)) * kLn2f;
+          }
         }
       }
-    __syncthreads();
-    const bool starts = t0 == 0, ends = t1 == it.tiles;
-    float* slot = slots + (starts ? slot_floats<D, NT>() : 0);
-    for (int i = tid; i < ROWS * (D / 2); i += C::kThreads) {
-      const int r = i / (D / 2), x = 2 * (i - r * (D / 2));
-      if (r >= rows) break;
-      float a0 = 0.f, a1 = 0.f, top = kNegBig, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        a0 += red[(w * ROWS + r) * C::kRedRow + x];
-        a1 += red[(w * ROWS + r) * C::kRedRow + x + 1];
-        top = fmaxf(top, sm_m[w * ROWS + r]);
-      }
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) sum += sm_l[w * ROWS + r] * ex2_approx(sm_m[w * ROWS + r] - top);
-      if (starts && ends) {
-        const int q = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - q * p.G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (it.q0 + q) * p.o_sn + hq * p.o_sh + x) =
-            pack_bf16x2(a0 * inv, a1 * inv);
-        if (x == 0 && p.lse != nullptr)
-          p.lse[static_cast<long long>(hq) * p.total_q + it.q0 + q] =
-              sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-      } else {
-        *reinterpret_cast<float2*>(slot + r * D + x) = make_float2(a0, a1);
-        if (x == 0) {
-          slot[ROWS * D + r] = top;
-          slot[ROWS * D + ROWS + r] = sum;
-        }
+    if (lane == 0) {
+      Meta& mt = metas[warp];
+      if (starts && !ends) {
+        mt.tail_valid = 1;
+        mt.b = it.b, mt.h = it.h, mt.chunk = it.chunk;
+        mt.rows[0] = rows;
+      } else if (!starts) {
+        mt.head_valid = 1;
+        mt.head_ends = ends;
+        mt.rows[1] = rows;
       }
     }
-    if (starts && !ends) tail_valid = true;
-    if (!starts) {
-      head_valid = true;
-      head_ends = ends;
-    }
-    __syncthreads();
+    __syncwarp();
   }
-  if (tid == 0)
-    *meta = Meta{tail_valid, it.b, it.h, it.chunk, head_valid, head_ends, {0, 0}};
+  __syncthreads();
+
+  // ---- join the parts of this block's warps, which follow one another ---------------------------------------
+  float* first_part = warp_parts - static_cast<size_t>(warp) * 2 * part_floats<D, NT>();
+  Meta mine_all{};
+  for (int w = -1; w < C::kWarps;) {
+    // a chunk from warp w's tail (w = -1: from the warps before this block) over the heads of the next ones
+    if (w >= 0 && !metas[w].tail_valid) {
+      ++w;
+      continue;
+    }
+    int last = w;
+    bool ended = false;
+    while (last + 1 < C::kWarps && !ended && metas[last + 1].head_valid) ended = metas[++last].head_ends;
+    if (last == w && w < 0) {  // no chunk from before
+      ++w;
+      continue;
+    }
+    const Meta& mt = metas[w < 0 ? 0 : w];
+    const int rows = w < 0 ? mt.rows[1] : mt.rows[0];
+    const bool done = w >= 0 && ended;  // the chunk lies in this block
+    auto part = [&](int j) { return first_part + (static_cast<size_t>(j) * 2 + (j == w ? 1 : 0)) * part_floats<D, NT>(); };
+    const int j0 = max(w, 0);
+    for (int i = tid; i < rows * (D / 2); i += C::kThreads) {
+      const int r = i / (D / 2), x = 2 * (i - r * (D / 2));
+      float top = kNegBig, a0 = 0.f, a1 = 0.f, sum = 0.f;
+      for (int j = j0; j <= last; ++j) top = fmaxf(top, part(j)[ROWS * D + r]);
+      for (int j = j0; j <= last; ++j) {
+        const float* q = part(j);
+        const float f = ex2_approx(q[ROWS * D + r] - top);
+        const float2 v = *reinterpret_cast<const float2*>(q + r * D + x);
+        a0 += v.x * f;
+        a1 += v.y * f;
+        sum += q[ROWS * D + ROWS + r] * f;
+      }
+      if (done) {
+        write_row_pair<D>(p, seq_len(p, mt.b).q0, mt.h, mt.chunk * ROWS + r, x, a0, a1, top, sum);
+      } else {
+        float* dst = block_parts + (w >= 0 ? part_floats<D, NT>() : 0);
+        *reinterpret_cast<float2*>(dst + r * D + x) = make_float2(a0, a1);
+        if (x == 0) {
+          dst[ROWS * D + r] = top;
+          dst[ROWS * D + ROWS + r] = sum;
+        }
+      }
+    }
+    if (w < 0) {
+      mine_all.head_valid = 1;
+      mine_all.head_ends = ended;
+    } else if (!ended) {
+      mine_all.tail_valid = 1;
+      mine_all.b = mt.b;
+      mine_all.h = mt.h;
+      mine_all.chunk = mt.chunk;
+    }
+    w = w < 0 ? (ended ? last : C::kWarps) : ended ? last : C::kWarps;
+    if (w < C::kWarps && !metas[w].tail_valid) ++w;
+  }
+  if (tid == 0) *meta = mine_all;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the parts of the row chunks that several blocks of threads share: block (i, r) does row r of
-// the chunk that starts in block i's span and goes on, in the order of the spans.
+// the chunk that starts in block i's span and goes on, in the order of the spans.  Its threads first look
+// together for the span where the chunk ends and for the largest m; then each adds two dimensions over
+// its share of the parts, whose loads do not wait for one another.
+constexpr int kJoinThreads = 128;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(D / 2) kv4_join_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnParams p) {
   constexpr int ROWS = 8 * NT;
+  constexpr int kShares = kJoinThreads / (D / 2);
+  __shared__ int s_last;
+  __shared__ float s_top[kJoinThreads / 32];
+  __shared__ float s_part[kShares][D / 2][3];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Meta* metas = reinterpret_cast<const Meta*>(p.ws);
-  const Meta mt = metas[blockIdx.x];
+  const int first = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const Meta mt = metas[first];
   if (!mt.tail_valid) return;
-  const float* parts = reinterpret_cast<const float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
   const SeqLen s = seq_len(p, mt.b);
-  const int row = mt.chunk * ROWS + blockIdx.y, r = blockIdx.y;
+  const int row = mt.chunk * ROWS + r;
   if (row >= s.nq * p.G) return;
-  int last = blockIdx.x + 1;
-  while (last < static_cast<int>(gridDim.x) - 1 && !metas[last].head_ends) ++last;
-  auto part = [&](int j) {
-    return parts + (static_cast<size_t>(j) * 2 + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * slot_floats<D, NT>();
+  if (tid == 0) s_last = gridDim.x - 1;
+  for (int base = first + 1;; base += kJoinThreads) {
+    const int j = base + tid;
+    const bool end = j >= static_cast<int>(gridDim.x) || metas[j].head_ends;
+    if (__syncthreads_or(end)) {
+      if (end) atomicMin(&s_last, j);
+      break;
+    }
+  }
+  __syncthreads();
+  const int last = s_last;
+  const float* parts = reinterpret_cast<const float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
+  auto part = [&](int j) {  // the first span holds the chunk in its second slot, the others in their first
+    return parts + (static_cast<size_t>(j) * 2 + (j == first ? 1 : 0)) * part_floats<D, NT>();
   };
   float top = kNegBig;
-  for (int j = blockIdx.x; j <= last; ++j) top = fmaxf(top, part(j)[ROWS * D + r]);
+  for (int j = first + tid; j <= last; j += kJoinThreads) top = fmaxf(top, part(j)[ROWS * D + r]);
+#pragma unroll
+  for (int sft = 16; sft; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
+  if ((tid & 31) == 0) s_top[tid >> 5] = top;
+  __syncthreads();
+  top = s_top[0];
+#pragma unroll
+  for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+  const int x = tid % (D / 2), share = tid / (D / 2);
   float a0 = 0.f, a1 = 0.f, sum = 0.f;
-  for (int j = blockIdx.x; j <= last; ++j) {
+#pragma unroll 4
+  for (int j = first + share; j <= last; j += kShares) {
     const float* q = part(j);
     const float f = ex2_approx(q[ROWS * D + r] - top);
-    const float2 v = *reinterpret_cast<const float2*>(q + r * D + 2 * threadIdx.x);
+    const float2 v = *reinterpret_cast<const float2*>(q + r * D + 2 * x);
     a0 += v.x * f;
     a1 += v.y * f;
     sum += q[ROWS * D + ROWS + r] * f;
   }
-  const int q = row / p.G, hq = mt.h * p.G + row - q * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (s.q0 + q) * p.o_sn + hq * p.o_sh + 2 * threadIdx.x) =
-      pack_bf16x2(a0 * inv, a1 * inv);
-  if (threadIdx.x == 0 && p.lse != nullptr)
-    p.lse[static_cast<long long>(hq) * p.total_q + s.q0 + q] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
+  if constexpr (kShares > 1) {
+    s_part[share][x][0] = a0;
+    s_part[share][x][1] = a1;
+    s_part[share][x][2] = sum;
+    __syncthreads();
+    if (share != 0) return;
+#pragma unroll
+    for (int i = 1; i < kShares; ++i) {
+      a0 += s_part[i][x][0];
+      a1 += s_part[i][x][1];
+      sum += s_part[i][x][2];
+    }
+  }
+  write_row_pair<D>(p, s.q0, mt.h, row, 2 * x, a0, a1, top, sum);
 }
 
 template <int D, int NT>
 unsigned long long ws_bytes(int num_sms) {
   const unsigned long long blocks = static_cast<unsigned long long>(num_sms) * SplitCfg<D, NT>::kBlocksPerSm;
-  return blocks * (sizeof(Meta) + 2 * sizeof(float) * slot_floats<D, NT>());
+  return blocks * (sizeof(Meta) + (2 + 2 * SplitCfg<D, NT>::kWarps) * sizeof(float) * part_floats<D, NT>());
 }
 
 template <int D, int NT>
@@ -792,7 +1021,7 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(grid, C::kRows);
-  cfg.blockDim = dim3(D / 2);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, p);
 }

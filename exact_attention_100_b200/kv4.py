@@ -18,11 +18,12 @@ With ``stream`` the call runs on that stream, and the tensors it makes belong to
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
-from . import (ATTN_BF16, ATTN_FP32, _check, _out, _ptr, _signs, _stream_ptr, _workspace, lib)
+from . import ATTN_BF16, ATTN_FP32, _check, lib
+
+_LL4, _LL12 = ctypes.c_longlong * 4, ctypes.c_longlong * 12
 
 
 def declare(L) -> None:
@@ -43,24 +44,58 @@ def declare(L) -> None:
     L.attn_fwd_kv4.restype = i
 
 
-def _on(stream):
-    """The stream that a call's own tensors are made on (and whose device is then the current one)."""
-    import torch
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+# A decode step calls each of these once per layer for a few microseconds of GPU work, so the checks
+# below are written to cost little: one look at the current device per call, plain attribute
+# comparisons per tensor, integers handed to ctypes.
+
+def _arg(t, shape, dtype, what, dev):
+    """Address of a contiguous tensor of this shape and type on the current device."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
 
 
-def _ints(t, shape, what):
-    import torch
-    return _out(t, shape, (torch.int32,), what)
+def _rows(t, shape, dtypes, what, dev):
+    """Address of a tensor whose last dimension is contiguous, the others by their strides."""
+    if t.shape != shape or t.dtype not in dtypes or t.stride(-1) != 1:
+        names = "/".join(str(x).replace("torch.", "") for x in dtypes)
+        raise ValueError(f"{what} must be {names} of shape {tuple(shape)} with a contiguous last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
 
 
-def _strides(*values):
-    a = (ctypes.c_longlong * len(values))(*[int(v) for v in values])
-    return ctypes.cast(a, ctypes.c_void_p)
+def _device(torch, *tensors):
+    """The current CUDA device; host tensors are refused before CUDA is asked for it."""
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError(f"a {tuple(t.shape)} tensor is on {t.device}, not on the current CUDA device")
+    return torch.cuda.current_device()
 
 
+def _on_stream(f):
+    """With ``stream``: runs the call with that stream current, so that the tensors it makes belong to it."""
+    import functools
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _raw_stream(torch, dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+@_on_stream
 def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, total, slots=None, positions=None,
-                   cu_seqlens=None, lens_out=None, cursor_out=None, stream=None):
+                   cu_seqlens=None, lens_out=None, cursor_out=None):
     """Block tables and slot maps of one serving step, on the GPU.
 
     ``lens``, ``new_lens`` [B] int32: tokens each request holds, and adds now; ``block_table``
@@ -71,84 +106,84 @@ def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, 
     not suffice is not served: its slots are -1 and its length stays.
     """
     import torch
-    B = int(lens.shape[0]) if lens.dim() == 1 else 0
-    if B == 0 or block_table.dim() != 2 or free_blocks.dim() != 1:
+    if lens.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1 or lens.shape[0] == 0:
         raise ValueError("expected lens [B], block_table [B, width], free_blocks [n]")
-    width, total = int(block_table.shape[1]), int(total)
-    _ints(lens, (B,), "lens")
-    _ints(new_lens, (B,), "new_lens")
-    _ints(block_table, (B, width), "block_table")
-    _ints(free_blocks, tuple(free_blocks.shape), "free_blocks")
-    _ints(cursor, (1,), "cursor")
+    B, width, n_free, total = lens.shape[0], block_table.shape[1], free_blocks.shape[0], int(total)
     if total < 0:
         raise ValueError("total must not be negative")
-    with _on(stream):
-        new = lambda t, n: t if t is not None else torch.empty(n, dtype=torch.int32, device=lens.device)
-        slots, positions = new(slots, total), new(positions, total)
-        cu_seqlens, lens_out, cursor_out = new(cu_seqlens, B + 1), new(lens_out, B), new(cursor_out, 1)
-        for t, n, what in ((slots, total, "slots"), (positions, total, "positions"), (cu_seqlens, B + 1, "cu_seqlens"),
-                           (lens_out, B, "lens_out"), (cursor_out, 1, "cursor_out")):
-            _ints(t, (n,), what)
-        _check(lib().attn_kv_tables(_ptr(lens), _ptr(new_lens), _ptr(block_table), _ptr(free_blocks), _ptr(cursor),
-                                    _ptr(slots), _ptr(positions), _ptr(cu_seqlens), _ptr(lens_out), _ptr(cursor_out), B,
-                                    width, int(page_size), int(free_blocks.shape[0]), total, _stream_ptr(stream)),
-               "attn_kv_tables")
+    dev, i32 = _device(torch, lens), torch.int32
+    ins = (_arg(lens, (B,), i32, "lens", dev), _arg(new_lens, (B,), i32, "new_lens", dev),
+           _arg(block_table, (B, width), i32, "block_table", dev), _arg(free_blocks, (n_free,), i32, "free_blocks", dev),
+           _arg(cursor, (1,), i32, "cursor", dev))
+    if slots is None and positions is None and cu_seqlens is None and lens_out is None and cursor_out is None:
+        # one allocation for the five
+        slots, positions, cu_seqlens, lens_out, cursor_out = lens.new_empty(2 * total + 2 * B + 2).split(
+            (total, total, B + 1, B, 1))
+    slots = slots if slots is not None else lens.new_empty(total)
+    positions = positions if positions is not None else lens.new_empty(total)
+    cu_seqlens = cu_seqlens if cu_seqlens is not None else lens.new_empty(B + 1)
+    lens_out = lens_out if lens_out is not None else lens.new_empty(B)
+    cursor_out = cursor_out if cursor_out is not None else lens.new_empty(1)
+    _check(lib().attn_kv_tables(*ins, _arg(slots, (total,), i32, "slots", dev),
+                                _arg(positions, (total,), i32, "positions", dev),
+                                _arg(cu_seqlens, (B + 1,), i32, "cu_seqlens", dev),
+                                _arg(lens_out, (B,), i32, "lens_out", dev), _arg(cursor_out, (1,), i32, "cursor_out", dev),
+                                B, width, int(page_size), n_free, total, _raw_stream(torch, dev)), "attn_kv_tables")
     return slots, positions, cu_seqlens, lens_out, cursor_out, block_table
 
 
-def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse, stream, name):
+def _dims(t):
+    """(B, heads, N, d) and (batch, head, row) strides of [tokens, heads, d] or [B, heads, N, d]."""
+    if t.dim() == 3:
+        (n, h, d), (sn, sh, _) = t.shape, t.stride()
+        return (1, h, n, d), (8, sh, sn)
+    return tuple(t.shape), t.stride()[:3]
+
+
+def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse, name):
     import torch
-    sections = [int(s) for s in sections]
+    f32 = torch.float32
+    types = (torch.bfloat16, f32)
     half = sum(sections)
     if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
         raise ValueError("q and k must be [tokens, heads, d] or [B, heads, N, d]")
-    packed = q.dim() == 3
-    dims = lambda t: (1, int(t.shape[1]), int(t.shape[0]), int(t.shape[2])) if packed else tuple(int(x) for x in t.shape)
-    st = lambda t: (8, t.stride(1), t.stride(0)) if packed else t.stride()[:3]
-    B, Hq, N, d = dims(q)
-    if k is not None and (dims(k)[0], dims(k)[2], dims(k)[3]) != (B, N, d):
-        raise ValueError("k must have q's tokens and d")
-    if k is not None and k.dtype != q.dtype:
-        raise ValueError("q and k must have one dtype")
-    types = (torch.bfloat16, torch.float32)
-    for t, what in ((q, "q"), (k, "k")):
-        if t is not None:
-            _out(t, tuple(t.shape), types, what, strided=True)
-    for t, what in ((cos, "cos"), (sin, "sin")):
-        if t.dim() != 2 or t.shape[0] == 0:
-            raise ValueError("cos and sin must be float32 [n_pos, sum of the sections]")
-        _out(t, (int(cos.shape[0]), half), (torch.float32,), what)
-    if positions.dim() == 1 and packed and len(sections) == 1:
+    if cos.dim() != 2 or cos.shape[0] == 0:
+        raise ValueError("cos and sin must be float32 [n_pos, sum of the sections]")
+    dev = _device(torch, q)
+    (B, Hq, N, d), strides_q = _dims(q)
+    pq = _rows(q, q.shape, types, "q", dev)
+    tables = _arg(cos, (cos.shape[0], half), f32, "cos", dev), _arg(sin, (cos.shape[0], half), f32, "sin", dev)
+    if positions.dim() == 1 and q.dim() == 3 and len(sections) == 1:
         positions = positions[None]
-    _ints(positions, (len(sections), N) if packed else (len(sections), B, N), "positions")
-    with _on(stream):
-        outs = []
-        for x, y, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if x is None:
-                if y is not None:
-                    raise ValueError("k_out without k")
-                outs.append(None)
-                continue
-            if y is None:
-                y = torch.empty_like(x, dtype=out_dtype or x.dtype)
-            outs.append(_out(y, tuple(x.shape), types, what, strided=True))
-        q_out, k_out = outs
-        if k_out is not None and k_out.dtype != q_out.dtype:
-            raise ValueError("q_out and k_out must have one dtype")
-        if B * N == 0 or Hq == 0:
-            return q_out, k_out
-        one = (8, 8, 8)
-        strides = _strides(*st(q), *(st(k) if k is not None else one), *st(q_out), *(st(k_out) if k is not None else one))
-        sec = (ctypes.c_int * len(sections))(*sections)
-        code = lambda t: ATTN_FP32 if t.dtype == torch.float32 else ATTN_BF16
-        _check(lib().attn_rope_axes(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(cos), _ptr(sin), _ptr(positions), B,
-                                    Hq, dims(k)[1] if k is not None else 0, N, d, len(sections),
-                                    ctypes.cast(sec, ctypes.c_void_p), int(cos.shape[0]), strides, inverse, code(q),
-                                    code(q_out), _stream_ptr(stream)), name)
+    at = _arg(positions, (len(sections), N) if q.dim() == 3 else (len(sections), B, N), torch.int32, "positions", dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, dtype=out_dtype or q.dtype)
+    pqo = _rows(q_out, q.shape, types, "q_out", dev)
+    strides_k = strides_ko = (8, 8, 8)
+    Hk = pk = pko = 0
+    if k is not None:
+        (Bk, Hk, Nk, dk), strides_k = _dims(k)
+        if (Bk, Nk, dk) != (B, N, d):
+            raise ValueError("k must have q's tokens and d")
+        pk = _rows(k, k.shape, (q.dtype,), "k", dev)
+        if k_out is None:
+            k_out = torch.empty_like(k, dtype=q_out.dtype)
+        pko = _rows(k_out, k.shape, (q_out.dtype,), "k_out", dev)
+        strides_ko = _dims(k_out)[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if B == 0 or N == 0:
+        return q_out, k_out
+    _check(lib().attn_rope_axes(pq, pk, pqo, pko, *tables, at, B, Hq, Hk, N, d, len(sections),
+                                (ctypes.c_int * len(sections))(*sections), cos.shape[0],
+                                _LL12(*strides_q, *strides_k, *_dims(q_out)[1], *strides_ko), inverse,
+                                ATTN_FP32 if q.dtype is f32 else ATTN_BF16, ATTN_FP32 if q_out.dtype is f32 else ATTN_BF16,
+                                _raw_stream(torch, dev)), name)
     return q_out, k_out
 
 
-def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, out_dtype=None, stream=None):
+@_on_stream
+def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, out_dtype=None):
     """Rotary embedding of ``q`` and ``k`` (``k`` may be None) with one to four position axes.
 
     ``q``, ``k``: [tokens, heads, d] or [B, heads, N, d], bf16 or float32, last dimension contiguous;
@@ -156,13 +191,14 @@ def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, 
     ``positions`` int32 [axes, tokens] or [axes, B, N]; ``sections``: how many of the ``half`` pairs turn
     with each axis, in order.  Coordinates i and i + half form pair i; dimensions past 2 * half are
     copied.  ``q_out=q``, ``k_out=k`` rotate in place.  Returns ``(q_out, k_out)``."""
-    return _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, 0, stream, "attn_rope_axes")
+    return _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, 0, "attn_rope_axes")
 
 
-def attn_rope_axes_bwd(dq, dk, cos, sin, positions, sections, dq_out=None, dk_out=None, out_dtype=None, stream=None):
+@_on_stream
+def attn_rope_axes_bwd(dq, dk, cos, sin, positions, sections, dq_out=None, dk_out=None, out_dtype=None):
     """The backward of :func:`attn_rope_axes`: gradients of its outputs to gradients of its inputs
     (bf16 or float32 each), with the same tables, positions and sections."""
-    return _rope(dq, dk, cos, sin, positions, sections, dq_out, dk_out, out_dtype, 1, stream, "attn_rope_axes_bwd")
+    return _rope(dq, dk, cos, sin, positions, sections, dq_out, dk_out, out_dtype, 1, "attn_rope_axes_bwd")
 
 
 def attn_kv4_cache(num_blocks, Hk, page_size, d, device=None):
@@ -175,56 +211,57 @@ def attn_kv4_cache(num_blocks, Hk, page_size, d, device=None):
                        device=device if device is not None else torch.device("cuda", torch.cuda.current_device()))
 
 
-def _cache_dims(cache):
-    """(num_blocks, Hk, page_size, d) of a cache."""
-    import torch
-    if cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.shape[3] % 18:
+def _cache_dims(cache, torch, dev):
+    """(num_blocks, Hk, page_size, d) of a cache, and its address."""
+    if cache.dim() != 4 or cache.shape[3] % 18:
         raise ValueError("cache must be contiguous uint8 [num_blocks, Hk, page / 16, 18 d]")
-    nb, hk, tiles, tile = (int(x) for x in cache.shape)
-    return nb, hk, 16 * tiles, tile // 18
+    nb, hk, tiles, tile = cache.shape
+    return nb, hk, 16 * tiles, tile // 18, _arg(cache, cache.shape, torch.uint8, "cache", dev)
 
 
-def attn_kv4_append(k, v, cache, slots, signs=None, stream=None):
+def _sign_arg(signs, d, torch, dev):
+    return _arg(signs, (d,), torch.int8, "signs", dev) if signs is not None else 0
+
+
+@_on_stream
+def attn_kv4_append(k, v, cache, slots, signs=None):
     """Quantises ``k``, ``v`` [T, Hk, d] bf16 (row and head strides free) to 4 bits and writes them to
     ``slots`` [T] int32 of ``cache``, in place (slot -1: skipped).  ``signs`` (d int8 entries +-1) puts
     K through the random-sign Hadamard transform first; give the same to :func:`attn_fwd_kv4`.
     Returns ``cache``."""
     import torch
-    nb, Hk, page, d = _cache_dims(cache)
-    T = int(slots.shape[0]) if slots.dim() == 1 else -1
-    _ints(slots, (T,), "slots")
-    for t, what in ((k, "k"), (v, "v")):
-        _out(t, (T, Hk, d), (torch.bfloat16,), what, strided=True)
-    if T == 0:
-        return cache
-    with _on(stream):
-        _check(lib().attn_kv4_append(_ptr(k), _ptr(v), _ptr(cache), _ptr(slots), _ptr(_signs(signs, d)), T, Hk, d, page,
-                                     nb, _strides(*k.stride()[:2], *v.stride()[:2]), _stream_ptr(stream)),
-               "attn_kv4_append")
+    dev, bf16 = _device(torch, k), (torch.bfloat16,)
+    nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
+    T = k.shape[0]
+    pk, pv = _rows(k, (T, Hk, d), bf16, "k", dev), _rows(v, (T, Hk, d), bf16, "v", dev)
+    ps, pg = _arg(slots, (T,), torch.int32, "slots", dev), _sign_arg(signs, d, torch, dev)
+    if T:
+        _check(lib().attn_kv4_append(pk, pv, pc, ps, pg, T, Hk, d, page, nb, _LL4(*k.stride()[:2], *v.stride()[:2]),
+                                     _raw_stream(torch, dev)), "attn_kv4_append")
     return cache
 
 
-def attn_kv4_read(cache, slots, k=None, v=None, dtype=None, stream=None):
+@_on_stream
+def attn_kv4_read(cache, slots, k=None, v=None, dtype=None):
     """The values held at ``slots`` [T] int32 of ``cache``: ``(k, v)`` [T, Hk, d] in ``dtype``
     (torch.bfloat16, the default, or torch.float32); slot -1 gives zeros.  A K that was transformed comes
     back transformed."""
     import torch
-    nb, Hk, page, d = _cache_dims(cache)
-    T = int(slots.shape[0]) if slots.dim() == 1 else -1
-    _ints(slots, (T,), "slots")
-    with _on(stream):
-        dt = dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
-        k = k if k is not None else torch.empty((T, Hk, d), dtype=dt, device=cache.device)
-        v = v if v is not None else torch.empty((T, Hk, d), dtype=dt, device=cache.device)
-        for t, what in ((k, "k"), (v, "v")):
-            _out(t, (T, Hk, d), (torch.bfloat16, torch.float32), what)
-        if k.dtype != v.dtype:
-            raise ValueError("k and v must have one dtype")
-        if T == 0:
-            return k, v
-        _check(lib().attn_kv4_read(_ptr(cache), _ptr(slots), _ptr(k), _ptr(v), T, Hk, d, page, nb,
-                                   ATTN_FP32 if k.dtype == torch.float32 else ATTN_BF16, _stream_ptr(stream)),
-               "attn_kv4_read")
+    dev = _device(torch, cache)
+    nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = slots.shape[0]
+    ps = _arg(slots, (T,), torch.int32, "slots", dev)
+    dt = dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError("the values are bf16 or float32")
+    k = k if k is not None else cache.new_empty((T, Hk, d), dtype=dt)
+    v = v if v is not None else cache.new_empty((T, Hk, d), dtype=dt)
+    pk, pv = _arg(k, (T, Hk, d), dt, "k", dev), _arg(v, (T, Hk, d), dt, "v", dev)
+    if T:
+        _check(lib().attn_kv4_read(pc, ps, pk, pv, T, Hk, d, page, nb, ATTN_FP32 if dt is torch.float32 else ATTN_BF16,
+                                   _raw_stream(torch, dev)), "attn_kv4_read")
     return k, v
 
 
@@ -234,8 +271,9 @@ def attn_fwd_kv4_workspace_bytes(d, num_sms=0) -> int:
     return int(lib().attn_fwd_kv4_workspace_bytes(int(d), int(num_sms)))
 
 
+@_on_stream
 def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_q=1, o=None, lse=None, workspace=None,
-                 signs=None, scale=None, causal=True, stream=None, want_lse=True):
+                 signs=None, scale=None, causal=True, want_lse=True):
     """Attention of ``q`` [total_q, Hq, d] bf16 (row and head strides free) over the 4-bit ``cache``,
     query head h reading key/value head ``h // (Hq // Hk)``.
 
@@ -247,35 +285,39 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
     float32)``; rows behind the last request are left as they were.
     """
     import torch
-    nb, Hk, page, d = _cache_dims(cache)
-    if q.dim() != 3 or int(q.shape[2]) != d or int(q.shape[1]) % Hk:
+    dev, i32, bf16 = _device(torch, q), torch.int32, (torch.bfloat16,)
+    nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
+    if q.dim() != 3 or q.shape[2] != d or q.shape[1] % Hk:
         raise ValueError("q must be [total_q, Hq, d] with the cache's d and a multiple of its heads")
-    total_q, Hq = int(q.shape[0]), int(q.shape[1])
-    _out(q, (total_q, Hq, d), (torch.bfloat16,), "q", strided=True)
-    if block_table.dim() != 2 or int(block_table.shape[0]) == 0:
+    if block_table.dim() != 2 or block_table.shape[0] == 0:
         raise ValueError("block_table must be [B, width]")
-    B, width = (int(x) for x in block_table.shape)
-    _ints(block_table, (B, width), "block_table")
-    _ints(seq_lens, (B,), "seq_lens")
+    total_q, Hq, _ = q.shape
+    B, width = block_table.shape
+    pq = _rows(q, q.shape, bf16, "q", dev)
+    pt = _arg(block_table, (B, width), i32, "block_table", dev)
+    pl = _arg(seq_lens, (B,), i32, "seq_lens", dev)
+    pcu = 0
     if cu_seqlens_q is not None:
-        _ints(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
-    elif total_q != B or int(max_seqlen_q) != 1:
+        pcu = _arg(cu_seqlens_q, (B + 1,), i32, "cu_seqlens_q", dev)
+    elif total_q != B or max_seqlen_q != 1:
         raise ValueError("without cu_seqlens_q there is one query per request")
-    with _on(stream):
-        if o is None:
-            o = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=q.device)
-        _out(o, (total_q, Hq, d), (torch.bfloat16,), "o", strided=True)
-        if lse is None and want_lse:
-            lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
-        if lse is not None:
-            _out(lse, (Hq, total_q), (torch.float32,), "lse")
-        if total_q == 0:
-            return o, lse
-        args = [_ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q), _ptr(o), _ptr(lse)]
-        nbytes = attn_fwd_kv4_workspace_bytes(d)
-        workspace = _workspace(workspace, nbytes, q.device, "attn_fwd_kv4")
-        s = float(scale) if scale is not None else 1.0 / math.sqrt(d)
-        _check(lib().attn_fwd_kv4(*args, _ptr(workspace), _ptr(_signs(signs, d)), B, Hq, Hk, total_q, int(max_seqlen_q),
-                                  d, page, nb, width, _strides(*q.stride()[:2], *o.stride()[:2]), s,
-                                  int(bool(causal)), _stream_ptr(stream)), "attn_fwd_kv4")
+    pg = _sign_arg(signs, d, torch, dev)
+    if o is None:
+        o = q.new_empty((total_q, Hq, d))
+    po = _rows(o, (total_q, Hq, d), bf16, "o", dev)
+    if lse is None and want_lse:
+        lse = q.new_empty((Hq, total_q), dtype=torch.float32)
+    pe = _arg(lse, (Hq, total_q), torch.float32, "lse", dev) if lse is not None else 0
+    if total_q == 0:
+        return o, lse
+    L = lib()
+    nbytes = L.attn_fwd_kv4_workspace_bytes(d, 0)
+    if workspace is None:
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"attn_fwd_kv4: the workspace must be contiguous and have {nbytes} bytes")
+    pw = _arg(workspace, workspace.shape, workspace.dtype, "workspace", dev)
+    _check(L.attn_fwd_kv4(pq, pc, pt, pl, pcu, po, pe, pw, pg, B, Hq, Hk, total_q, int(max_seqlen_q), d, page, nb, width,
+                          _LL4(*q.stride()[:2], *o.stride()[:2]), float(scale) if scale is not None else 1.0 / math.sqrt(d),
+                          1 if causal else 0, _raw_stream(torch, dev)), "attn_fwd_kv4")
     return o, lse
