@@ -32,23 +32,13 @@
 // parts of its warps, which follow one another, and leaves at most two parts itself, of a chunk that began
 // before it and of one that goes on after it; the join kernel adds those, in order.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
-#include "attn_kernels.h"
-#include "kv4_format.cuh"
-#include "kv_kernels.h"
-#include "sm100_ptx.cuh"
+#include "kv4_attn.cuh"
 
 namespace ea {
 
 namespace {
-
-constexpr float kTau = 8.f;        // lazy maximum: p <= 2^kTau
-constexpr float kNegBig = -1e30f;  // below any score, and finite
-constexpr float kLn2f = 0.6931471805599453f;
 
 // Keys of a unit: two tiles, which share one wait, one vote and one round of copies (a tile at a time
 // took 421 instructions per tile, a quarter of them for those)
@@ -57,6 +47,8 @@ constexpr int kKeys = 32;
 constexpr int kChunkCost = 3;
 // A warp gets at least this much work: fewer spans than warps for short contexts, so that less is left to join
 constexpr int kMinCost = 2;
+// Requests of more rows per key/value head than this go to the chunk kernel (d = 64, 128)
+constexpr int kChunkMinRows = 32;
 // Units after which the sums of codes are centred
 constexpr int kCentre = 16;
 
@@ -77,27 +69,6 @@ struct SplitCfg {
   static_assert((kSmem + 3072) * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
 };
 
-// A part of a chunk: [kRows][D] float O, [kRows] m, [kRows] l.  The workspace holds per block of threads a Meta
-// and two parts (of the chunk that began before it, then of the one that goes on after it), then two parts
-// per warp, likewise.
-template <int D, int NT>
-__host__ __device__ constexpr int part_floats() { return 8 * NT * (D + 2); }
-
-struct Meta {
-  int tail_valid;  // the last chunk starts here and goes on behind
-  int b, h, chunk;
-  int head_valid;  // the first chunk started before
-  int head_ends;   // ... and ends here
-  int rows[2];     // of the tail, of the head (a warp's)
-};
-
-// A part of a row chunk of one request and key/value head: its units [t0, t1) of `units`.
-struct Segment {
-  int b, h, chunk;
-  int nq, nk, q0;
-  int units, t0, t1;
-};
-
 // Where a walk over a span's segments stands.
 struct Walk {
   long long pos;    // next position of the span
@@ -106,30 +77,6 @@ struct Walk {
   long long cost;   // of request b, -1: not looked up yet
   int b;
 };
-
-struct SeqLen {
-  int nq, nk, q0;
-  bool bad;
-};
-
-__device__ __forceinline__ SeqLen seq_len(const Kv4AttnParams& p, int b) {
-  SeqLen s;
-  int q0 = b, q1 = b + 1;
-  if (p.cu_q != nullptr) {
-    q0 = __ldg(p.cu_q + b);
-    q1 = __ldg(p.cu_q + b + 1);
-  }
-  const int nk = __ldg(p.lens + b);
-  s.bad = !(0 <= q0 && q0 <= q1 && q1 <= p.total_q && q1 - q0 <= p.max_q && nk >= 0 &&
-            nk <= static_cast<long long>(p.width) * p.page);
-  s.nq = s.bad ? 0 : q1 - q0;
-  s.nk = s.bad ? 0 : nk;
-  s.q0 = q0;
-  // requests of the other launch
-  const long long rows = static_cast<long long>(s.nq) * p.G;
-  if (rows <= p.min_rows || rows > p.max_rows) s.nq = 0;
-  return s;
-}
 
 // Units of one row chunk of a request (one, with every key masked, where it has no key).
 __device__ __forceinline__ int chunk_units(int nk) { return nk > 0 ? (nk + kKeys - 1) / kKeys : 1; }
@@ -199,36 +146,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// 2^e for -126 <= e <= 127
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
-
-// After a wait that ran out: waits for the stage's copy all the same (as long again), so that none
-// lands after the block has ended.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_timer_ns();
-  while (!bar_try_wait(smem_addr(bar), parity))
-    if (global_timer_ns() - t0 > kWaitLimitNs) return;
-}
-
-// Writes dimensions x, x + 1 of O (a0, a1 over sum) of a request's row, and with x = 0 its LSE.
-template <int D>
-__device__ __forceinline__ void write_row_pair(const Kv4AttnParams& p, int q0, int h, int row, int x, float a0, float a1,
-                                               float top, float sum) {
-  const int i = row / p.G, hq = h * p.G + row - i * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (q0 + i) * p.o_sn + hq * p.o_sh + x) =
-      pack_bf16x2(a0 * inv, a1 * inv);
-  if (x == 0 && p.lse != nullptr)
-    p.lse[static_cast<long long>(hq) * p.total_q + q0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
 }
 
 // Key of the tile that sits at index a of the products' key side: an order in which the rows that a
@@ -314,9 +231,9 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
 
   const AbortState ab{&abort_flag, p.status};
   float* block_parts = reinterpret_cast<float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
-  float* warp_parts = block_parts + static_cast<size_t>(gridDim.x) * 2 * part_floats<D, NT>() +
-                      (static_cast<size_t>(blockIdx.x) * C::kWarps + warp) * 2 * part_floats<D, NT>();
-  block_parts += static_cast<size_t>(blockIdx.x) * 2 * part_floats<D, NT>();
+  float* warp_parts = block_parts + static_cast<size_t>(gridDim.x) * 2 * part_floats<D, ROWS>() +
+                      (static_cast<size_t>(blockIdx.x) * C::kWarps + warp) * 2 * part_floats<D, ROWS>();
+  block_parts += static_cast<size_t>(blockIdx.x) * 2 * part_floats<D, ROWS>();
 
   // ---- producer side: the units of the span, in order; segments go into the warp's queue --------------
   int p_seg = -1;            // segments opened, less one
@@ -813,7 +730,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
         const bool whole_chunk = starts && ends;
         const float inv = whole_chunk ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         const int i = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - i * p.G;
-        float* part = warp_parts + (starts ? part_floats<D, NT>() : 0);
+        float* part = warp_parts + (starts ? part_floats<D, ROWS>() : 0);
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
           float z = zacc[nt][gr][e];
@@ -864,7 +781,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   __syncthreads();
 
   // ---- join the parts of this block's warps, which follow one another ---------------------------------------
-  float* first_part = warp_parts - static_cast<size_t>(warp) * 2 * part_floats<D, NT>();
+  float* first_part = warp_parts - static_cast<size_t>(warp) * 2 * part_floats<D, ROWS>();
   Meta mine_all{};
   for (int w = -1; w < C::kWarps;) {
     // a chunk from warp w's tail (w = -1: from the warps before this block) over the heads of the next ones
@@ -882,7 +799,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     const Meta& mt = metas[w < 0 ? 0 : w];
     const int rows = w < 0 ? mt.rows[1] : mt.rows[0];
     const bool done = w >= 0 && ended;  // the chunk lies in this block
-    auto part = [&](int j) { return first_part + (static_cast<size_t>(j) * 2 + (j == w ? 1 : 0)) * part_floats<D, NT>(); };
+    auto part = [&](int j) { return first_part + (static_cast<size_t>(j) * 2 + (j == w ? 1 : 0)) * part_floats<D, ROWS>(); };
     const int j0 = max(w, 0);
     for (int i = tid; i < rows * (D / 2); i += C::kThreads) {
       const int r = i / (D / 2), x = 2 * (i - r * (D / 2));
@@ -899,7 +816,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
       if (done) {
         write_row_pair<D>(p, seq_len(p, mt.b).q0, mt.h, mt.chunk * ROWS + r, x, a0, a1, top, sum);
       } else {
-        float* dst = block_parts + (w >= 0 ? part_floats<D, NT>() : 0);
+        float* dst = block_parts + (w >= 0 ? part_floats<D, ROWS>() : 0);
         *reinterpret_cast<float2*>(dst + r * D + x) = make_float2(a0, a1);
         if (x == 0) {
           dst[ROWS * D + r] = top;
@@ -923,82 +840,12 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the parts of the row chunks that several blocks of threads share: block (i, r) does row r of
-// the chunk that starts in block i's span and goes on, in the order of the spans.  Its threads first look
-// together for the span where the chunk ends and for the largest m; then each adds two dimensions over
-// its share of the parts, whose loads do not wait for one another.
-constexpr int kJoinThreads = 128;
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnParams p) {
-  constexpr int ROWS = 8 * NT;
-  constexpr int kShares = kJoinThreads / (D / 2);
-  __shared__ int s_last;
-  __shared__ float s_top[kJoinThreads / 32];
-  __shared__ float s_part[kShares][D / 2][3];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Meta* metas = reinterpret_cast<const Meta*>(p.ws);
-  const int first = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
-  const Meta mt = metas[first];
-  if (!mt.tail_valid) return;
-  const SeqLen s = seq_len(p, mt.b);
-  const int row = mt.chunk * ROWS + r;
-  if (row >= s.nq * p.G) return;
-  if (tid == 0) s_last = gridDim.x - 1;
-  for (int base = first + 1;; base += kJoinThreads) {
-    const int j = base + tid;
-    const bool end = j >= static_cast<int>(gridDim.x) || metas[j].head_ends;
-    if (__syncthreads_or(end)) {
-      if (end) atomicMin(&s_last, j);
-      break;
-    }
-  }
-  __syncthreads();
-  const int last = s_last;
-  const float* parts = reinterpret_cast<const float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
-  auto part = [&](int j) {  // the first span holds the chunk in its second slot, the others in their first
-    return parts + (static_cast<size_t>(j) * 2 + (j == first ? 1 : 0)) * part_floats<D, NT>();
-  };
-  float top = kNegBig;
-  for (int j = first + tid; j <= last; j += kJoinThreads) top = fmaxf(top, part(j)[ROWS * D + r]);
-#pragma unroll
-  for (int sft = 16; sft; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
-  if ((tid & 31) == 0) s_top[tid >> 5] = top;
-  __syncthreads();
-  top = s_top[0];
-#pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-  const int x = tid % (D / 2), share = tid / (D / 2);
-  float a0 = 0.f, a1 = 0.f, sum = 0.f;
-#pragma unroll 4
-  for (int j = first + share; j <= last; j += kShares) {
-    const float* q = part(j);
-    const float f = ex2_approx(q[ROWS * D + r] - top);
-    const float2 v = *reinterpret_cast<const float2*>(q + r * D + 2 * x);
-    a0 += v.x * f;
-    a1 += v.y * f;
-    sum += q[ROWS * D + ROWS + r] * f;
-  }
-  if constexpr (kShares > 1) {
-    s_part[share][x][0] = a0;
-    s_part[share][x][1] = a1;
-    s_part[share][x][2] = sum;
-    __syncthreads();
-    if (share != 0) return;
-#pragma unroll
-    for (int i = 1; i < kShares; ++i) {
-      a0 += s_part[i][x][0];
-      a1 += s_part[i][x][1];
-      sum += s_part[i][x][2];
-    }
-  }
-  write_row_pair<D>(p, s.q0, mt.h, row, 2 * x, a0, a1, top, sum);
-}
-
+// The workspace: the blocks' parts, then two parts per warp, likewise.
 template <int D, int NT>
 unsigned long long ws_bytes(int num_sms) {
-  const unsigned long long blocks = static_cast<unsigned long long>(num_sms) * SplitCfg<D, NT>::kBlocksPerSm;
-  return blocks * (sizeof(Meta) + (2 + 2 * SplitCfg<D, NT>::kWarps) * sizeof(float) * part_floats<D, NT>());
+  using C = SplitCfg<D, NT>;
+  const unsigned long long blocks = static_cast<unsigned long long>(num_sms) * C::kBlocksPerSm;
+  return part_bytes<D, C::kRows>(blocks) + blocks * C::kWarps * 2 * sizeof(float) * part_floats<D, C::kRows>();
 }
 
 template <int D, int NT>
@@ -1014,16 +861,7 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   kv4_split_kernel<D, NT><<<grid, C::kThreads, C::kSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(grid, C::kRows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, p);
+  return launch_join<D, C::kRows>(p, grid, C::kRows, stream);
 }
 
 }  // namespace
@@ -1034,6 +872,7 @@ unsigned long long kv4_attn_workspace_bytes(int d, int num_sms) {
   if (d == 64) most(ws_bytes<64, 1>(num_sms)), most(ws_bytes<64, 2>(num_sms));
   if (d == 128) most(ws_bytes<128, 1>(num_sms)), most(ws_bytes<128, 2>(num_sms));
   if (d == 256) most(ws_bytes<256, 1>(num_sms));
+  most(kv4_chunk_workspace_bytes(d, num_sms));
   return n;
 }
 
@@ -1043,17 +882,28 @@ cudaError_t setup_kv4_attn_kernels() {
   if (e == cudaSuccess) e = setup<128, 1>();
   if (e == cudaSuccess) e = setup<128, 2>();
   if (e == cudaSuccess) e = setup<256, 1>();
+  if (e == cudaSuccess) e = setup_kv4_chunk_kernels();
   return e;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches) {
+  Kv4AttnParams few = p;
   *launches = 2;
+  if (d <= 128 && static_cast<long long>(p.max_q) * p.G > kChunkMinRows) {
+    // requests of many rows go to the chunk kernel, the others of the batch, if it has any, to this one; both
+    // write their parts into the same workspace, one after the other
+    Kv4AttnParams many = p;
+    many.min_rows = few.max_rows = p.B == 1 ? 0 : kChunkMinRows;  // a request alone: one kernel, whatever its rows
+    const cudaError_t e = launch_kv4_chunk(many, d, num_sms, stream);
+    if (e != cudaSuccess || p.B == 1) return e;
+    *launches = 4;
+  }
   // 8 rows on the small side of the products, or two sets of 8 for one pass over the keys where there
   // are more rows (not at d = 256, where O of 16 rows would fill the registers)
   const bool two = static_cast<long long>(p.max_q) * p.G > 8;
-  if (d == 64) return two ? launch<64, 2>(p, num_sms, stream) : launch<64, 1>(p, num_sms, stream);
-  if (d == 128) return two ? launch<128, 2>(p, num_sms, stream) : launch<128, 1>(p, num_sms, stream);
-  return launch<256, 1>(p, num_sms, stream);
+  if (d == 64) return two ? launch<64, 2>(few, num_sms, stream) : launch<64, 1>(few, num_sms, stream);
+  if (d == 128) return two ? launch<128, 2>(few, num_sms, stream) : launch<128, 1>(few, num_sms, stream);
+  return launch<256, 1>(few, num_sms, stream);
 }
 
 }  // namespace ea

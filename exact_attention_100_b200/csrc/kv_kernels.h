@@ -79,6 +79,10 @@ struct Kv4AttnParams {
 };
 unsigned long long kv4_attn_workspace_bytes(int d, int num_sms);
 cudaError_t setup_kv4_attn_kernels();
+// Requests of many rows (kv4_chunk.cu; d = 64, 128), called by launch_kv4_attn.
+cudaError_t setup_kv4_chunk_kernels();
+unsigned long long kv4_chunk_workspace_bytes(int d, int num_sms);
+cudaError_t launch_kv4_chunk(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches);
 
 }  // namespace ea

@@ -66,25 +66,36 @@ def reference(q, ks, vs, cu, ctx, scale, causal, signs=None):
                              None if signs is None else signs.cpu().numpy())
 
 
-def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref, q_step=0.0, k_step=0.0, p_step=2.0 ** -11,
-           v_step=0.0):
-    """Elementwise bounds on |O - ref| and |LSE - ref|, from first-order error propagation:
+# Requests with more rows (queries times heads per key/value head) than this, at d <= 128, go to the kernel
+# that brings K and V to float16
+FEW_ROWS = 32
 
-    a score s_j = scale q . k_j is off by at most d_j = scale (q_step + k_step + 2^-18) sum_i |q_i| |k_ji|
-    (relative roundings of q's and k's entries, and of float32 sums of up to 256 products whose codes
-    carry an offset, at most 16 times the value's own size, 2^-24 each) + 2^-20 |s_j| (scale factors, exp2);
-    LSE is then off by at most sum_j p_j d_j, O by sum_j p_j d_j |v_j - O|; p_j times V's step is rounded
-    by p_step, which moves O by p_step sum_j p_j (|v_j| + 15 s_j) <= p_step 3 sum_j p_j max|v_j| (a code times
-    its step is at most the range, twice the largest value); V's own rounding adds v_step sum_j p_j |v_j|;
+
+def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
+    """Elementwise bounds on |O - ref| and |LSE - ref|, from first-order error propagation.
+
+    A score s_j = scale q . k_j is off by at most d_j = scale e sum_i |q_i| |k_ji| + x |s_j| + x, with e the relative
+    roundings of q's and k's entries and of the sums, x those of the scale factors and the exponential.
+    LSE is then off by at most sum_j p_j d_j, O by sum_j p_j d_j |v_j - O|.
+    Few rows: q is kept in 22 bits and the codes are exact: e = 2^-21 + 2^-18 (float32 sums of up to 256 products
+    whose codes carry an offset, at most 16 times the value's own size, cut off at 2^-23 each), x = 2^-20; p_j times
+    V's step is rounded by 2^-11, which moves O by 2^-11 sum_j p_j (|v_j| + 15 s_j) <= 2^-11 3 sum_j p_j max|v_j| (a code
+    times its step is at most the range, twice the largest value).
+    Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18; the exponential of a quarter
+    of the keys is a cubic, off by 7.5e-5: x = 8e-5; V and p are rounded by 2^-11 each: 2^-10 sum_j p_j |v_j|.
     O is rounded to bf16, 2^-8.  Second order: the whole times 1.1."""
     q = q.float().cpu().numpy().astype(np.float64)
     if signs is not None:
         q = hadamard_f64(q, signs.cpu().numpy())
     ob, lb = np.full(o_ref.shape, np.inf), np.full(lse_ref.shape, np.inf)
+    group = q.shape[1] // ks[0].shape[1]
+    most = max((int(cu[b + 1]) - int(cu[b])) * group for b in range(len(ctx)))
     for b, n in enumerate(ctx):
         lo, hi = int(cu[b]), int(cu[b + 1])
+        many = q.shape[2] <= 128 and most > FEW_ROWS and ((hi - lo) * group > FEW_ROWS or len(ctx) == 1)
+        e, x = (2.0 ** -10 + 2.0 ** -18, 8e-5) if many else (2.0 ** -21 + 2.0 ** -18, 2.0 ** -20)
         for h in range(q.shape[1]):
-            kh = h // (q.shape[1] // ks[b].shape[1])
+            kh = h // group
             for i in range(lo, hi):
                 seen = max(0, n - (hi - lo) + (i - lo) + 1) if causal else n
                 if seen == 0:
@@ -93,19 +104,17 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref, q_step=0.0,
                 k, v = ks[b][:seen, kh], vs[b][:seen, kh]
                 s = scale * (k @ q[i, h])
                 p = np.exp(s - lse_ref[h, i])
-                dj = scale * (q_step + k_step + 2.0 ** -18) * (np.abs(k) @ np.abs(q[i, h])) + 2.0 ** -20 * np.abs(s)
+                dj = scale * e * (np.abs(k) @ np.abs(q[i, h])) + x * np.abs(s) + x
                 vmax = np.abs(v).max(-1, keepdims=True)
-                ob[i, h] = 1.1 * ((p * dj) @ np.abs(v - o_ref[i, h]) + (p_step * 3 * (p @ vmax))
-                                  + v_step * (p @ np.abs(v))) + 2.0 ** -8 * np.abs(o_ref[i, h])
+                round_p = 2.0 ** -10 * (p @ np.abs(v)) if many else 2.0 ** -11 * 3 * (p @ vmax)
+                ob[i, h] = 1.1 * ((p * dj) @ np.abs(v - o_ref[i, h]) + round_p) + 2.0 ** -8 * np.abs(o_ref[i, h])
                 lb[h, i] = 1.1 * (p @ dj) + 2.0 ** -22 * (abs(lse_ref[h, i]) + 8)
     return ob, lb
 
 
-def check(o, lse, q, ks, vs, cu, ctx, scale, causal, signs=None, **steps):
+def check(o, lse, q, ks, vs, cu, ctx, scale, causal, signs=None):
     o_ref, lse_ref = reference(q, ks, vs, cu, ctx, scale, causal, signs)
-    if signs is not None:
-        steps.setdefault("q_step", 2.0 ** -11)  # the transformed q in float16
-    ob, lb = bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref, **steps)
+    ob, lb = bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref)
     rows = int(cu[-1])
     o, lse = o.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
     worst = np.max(np.abs(o[:rows] - o_ref[:rows]) / (ob[:rows] + 1e-300))
