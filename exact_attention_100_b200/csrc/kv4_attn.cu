@@ -866,13 +866,16 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-unsigned long long kv4_attn_workspace_bytes(int d, int num_sms) {
+// Whether some request may go to the chunk kernel.
+bool may_chunk(long long max_q, int G, int d) { return d <= 128 && max_q * G > kChunkMinRows; }
+
+unsigned long long kv4_attn_workspace_bytes(int B, int Hk, int G, long long total_q, int max_q, int d, int num_sms) {
   unsigned long long n = 0;
   auto most = [&](unsigned long long v) { n = v > n ? v : n; };
   if (d == 64) most(ws_bytes<64, 1>(num_sms)), most(ws_bytes<64, 2>(num_sms));
   if (d == 128) most(ws_bytes<128, 1>(num_sms)), most(ws_bytes<128, 2>(num_sms));
   if (d == 256) most(ws_bytes<256, 1>(num_sms));
-  most(kv4_chunk_workspace_bytes(d, num_sms));
+  if (may_chunk(max_q, G, d)) most(kv4_chunk_workspace_bytes(B, Hk, G, total_q, d, num_sms));
   return n;
 }
 
@@ -889,14 +892,15 @@ cudaError_t setup_kv4_attn_kernels() {
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches) {
   Kv4AttnParams few = p;
   *launches = 2;
-  if (d <= 128 && static_cast<long long>(p.max_q) * p.G > kChunkMinRows) {
+  if (may_chunk(p.max_q, p.G, d)) {
     // requests of many rows go to the chunk kernel, the others of the batch, if it has any, to this one; both
     // write their parts into the same workspace, one after the other
     Kv4AttnParams many = p;
     many.min_rows = few.max_rows = p.B == 1 ? 0 : kChunkMinRows;  // a request alone: one kernel, whatever its rows
+    *launches = 3;
     const cudaError_t e = launch_kv4_chunk(many, d, num_sms, stream);
     if (e != cudaSuccess || p.B == 1) return e;
-    *launches = 4;
+    *launches = 5;
   }
   // 8 rows on the small side of the products, or two sets of 8 for one pass over the keys where there
   // are more rows (not at d = 256, where O of 16 rows would fill the registers)

@@ -6,21 +6,28 @@
 // Bound by arithmetic: 4 d flops per row and key for 1.125 d bytes per key, so the codes are brought to float16
 // in shared memory once per block and used by both tiles.
 //
-//   warps 0-3, 4-7   softmax of tile 0, 1: one thread per row.  Loads and transforms Q, and writes O.
-//   warps 8-11       codes to float16 K and V tiles (128-byte swizzle), 4 threads per key
-//   warp 12          one thread issues every tcgen05.mma
-//   warp 13          copies tiles of the cache (one bulk copy each) into a ring of shared memory
+//   warps 0-3, 4-7   softmax of tile 0, 1: one thread per row; writes O
+//   warps 8-15       codes of K to float16 tiles (128-byte swizzle), then those of V, 4 threads per key
+//   warp 16          one thread issues every tcgen05.mma
+//   warp 17          copies Q, and tiles of the cache (one bulk copy each) into a ring of three and a half blocks
+// K and V tiles take turns in three slots: V of a block is brought in while its S runs, K of the next one while
+// its P.V does.  Five warps of different roles share a scheduler, so each role's loop is kept short: with the loops
+// unrolled (160 KB of code) a third of the cycles went by without an instruction.
 //
 // Every operand is float16 (11 bits): Q, each row scaled by a power of two; K and V, u s + z in one fused
-// multiply-add, scaled by a power of two of the block's largest value (K) or the largest so far (V, O moves with
-// it as with the running maximum); P, at most 2^8.  A score is off by two roundings of 2^-11 per product (LSE
-// by 5e-6 of itself at unit inputs); with bf16 operands it would be eight times that.
+// multiply-add, scaled by a power of two that puts the block's largest value (K) or the largest so far (V, O moves
+// with it as with the running maximum) at 2^-8 .. 2^-7; P, at most 2^8.  A score is off by two roundings of 2^-11 per
+// product (LSE by 5e-6 of itself at unit inputs); with bf16 operands it would be eight times that.  At that size the
+// step times 2^24 is a float16, and a nibble masked in place (the subnormal u 2^-24, or 16 u 2^-24) goes straight into
+// the multiply-add; values under a 64th of the largest keep fewer bits, 2^-18 of the largest.
 //
 // A word of codes gives its nibbles in pairs (0, 4), (1, 5), (2, 6), (3, 7), so the 8 dimensions of a 16-byte chunk
 // lie in that order, in K and Q alike, and the columns of O are put back on the way out.
 //
 // Work is (request, chunk, kv head) after another in blocks of keys (those that some row of the chunk sees), cut
 // into equal spans, one per SM; parts are joined as for few rows (kv4_attn.cuh).
+
+#include <type_traits>
 
 #include "kv4_attn.cuh"
 
@@ -37,21 +44,20 @@ constexpr int kMinCost = 2;
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 576;
   static constexpr int kBoxes = D / 64;                 // 64-dimension halves, rows of 128 bytes
   static constexpr int kBoxBytes = 128 * 128;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;  // 128 rows x D float16
-  static constexpr int kRawSlots = 6;                   // pairs of the cache's tiles
+  static constexpr int kSlots = 3;                      // of K and V tiles, by turns
+  static constexpr int kRawSlots = 14;                  // pairs of the cache's tiles
   static constexpr int kRawBytes = 2 * Kv4Tile<D>::kBytes;
   static constexpr int kQOff = 0;
-  static constexpr int kKvOff = 2 * kTileBytes;         // K, V of block 0 mod 2, then of 1 mod 2
-  static constexpr int kRawOff = kKvOff + 4 * kTileBytes;
+  static constexpr int kKvOff = 2 * kTileBytes;
+  static constexpr int kRawOff = kKvOff + kSlots * kTileBytes;
   static constexpr int kSmem = kRawOff + kRawSlots * kRawBytes + 1024;  // room to align to 1024 bytes
   static constexpr int kOCol = 256;
   static constexpr int kTmemCols = 512;
   static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
-  static constexpr uint32_t kRegSoftmax = 168, kRegCodes = 96, kRegOther = 80;
-  static_assert((2 * kRegSoftmax + kRegCodes + kRegOther) * 128 == 65536, "register split");
 };
 
 // What the softmax needs to know of a block of keys
@@ -59,6 +65,7 @@ struct BlockInfo {
   float k_back;  // K was scaled by its inverse
   int v_exp;     // V was scaled by 2^-v_exp
   uint32_t gone;  // bit i: tile i of the block is not there (a table entry out of range)
+  uint32_t odd[4];  // one bit per key: its V is not finite (and is held as zero in shared memory)
 };
 
 struct ChunkWalk {
@@ -86,7 +93,7 @@ __device__ __forceinline__ long long request_cost(const Kv4AttnParams& p, const 
 
 // The next segment of a walk (one lane): false when the span has ended.  A boundary inside the cost in front
 // of a chunk counts as the chunk's start.
-__device__ __forceinline__ bool next_segment(const Kv4AttnParams& p, volatile ChunkWalk& w) {
+__device__ __noinline__ bool next_segment(const Kv4AttnParams& p, volatile ChunkWalk& w) {
   long long pos = w.pos, first = w.first;
   const long long end = w.end;
   int b = w.b, chunk = w.chunk, chunks = w.chunks;
@@ -134,29 +141,26 @@ __device__ __forceinline__ bool take_segment(const Kv4AttnParams& p, volatile Ch
   return true;
 }
 
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
-// The 8 codes of a word as float16 u s + z, in pairs (0, 4), (1, 5), (2, 6), (3, 7).  A nibble under the exponent of
-// 1024 is 1024 + u (or 1024 + 16 u): one exact addition (or multiply-add by 1/16) gives u.
-__device__ __forceinline__ uint4 expand(uint32_t w, uint32_t s2, uint32_t z2) {
-  constexpr uint32_t kMagic = 0x64006400u, kMinus1024 = 0xE400E400u, kSixteenth = 0x2C002C00u, kMinus64 = 0xD400D400u;
+// A group's (s, z) word as operands of expand: s 2^24 f, s 2^20 f and z f, each twice, in float16.
+struct Scales {
+  uint32_t s, s16, z;
+};
+__device__ __forceinline__ Scales scales_of(uint32_t w, float f) {
+  const float s = __uint_as_float(w << 16) * (f * 16777216.f), z = __uint_as_float(w & 0xFFFF0000u) * f;
+  return Scales{pack_f16x2(s, s), pack_f16x2(s * 0.0625f, s * 0.0625f), pack_f16x2(z, z)};
+}
+
+// The 8 codes of a word as float16 u s + z, in pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 expand(uint32_t w, const Scales& k) {
   const uint32_t h = w >> 8;
-  uint32_t a = (w & 0x000F000Fu) | kMagic, b = (w & 0x00F000F0u) | kMagic;
-  uint32_t c = (h & 0x000F000Fu) | kMagic, d = (h & 0x00F000F0u) | kMagic;
-  a = hadd2(a, kMinus1024);
-  b = hfma2(b, kSixteenth, kMinus64);
-  c = hadd2(c, kMinus1024);
-  d = hfma2(d, kSixteenth, kMinus64);
-  return make_uint4(hfma2(a, s2, z2), hfma2(b, s2, z2), hfma2(c, s2, z2), hfma2(d, s2, z2));
+  return make_uint4(hfma2(w & 0x000F000Fu, k.s, k.z), hfma2(w & 0x00F000F0u, k.s16, k.z),
+                    hfma2(h & 0x000F000Fu, k.s, k.z), hfma2(h & 0x00F000F0u, k.s16, k.z));
 }
 
 // (x0, x1) <- (s0 * c + nm, s1 * c + nm) and (a0, a1) += (b0, b1), packed
@@ -171,51 +175,136 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
       : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
 }
 
-// A row of S (128 columns of this thread's lane)
-__device__ __forceinline__ void load_row(uint32_t taddr, uint32_t (&r)[128]) {
-  tmem_ld_32cols(taddr, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-  tmem_ld_32cols(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-  tmem_ld_32cols(taddr + 64, *reinterpret_cast<uint32_t(*)[32]>(&r[64]));
-  tmem_ld_32cols(taddr + 96, *reinterpret_cast<uint32_t(*)[32]>(&r[96]));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 128; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
 }
 
-// p = 2^(s c + nm) of a row: packed float16 in pk, their sum returned.  A quarter of the exponentials of a block
-// that every row sees whole run on the FMA pipe, as in the bf16 forward.
-template <bool kMasked>
-__device__ __forceinline__ float softmax_row(uint32_t (&r)[128], uint32_t (&pk)[64], float c, float nm) {
-  float acc[8];
+// p = 2^(s c + nm) of 32 keys: packed float16 in pk, their sums added to acc; returns the largest of them as float16
+// (positive ones compare as their bits).  All exponentials on the special-function unit: 2,048 of its cycles per block
+// and scheduler; a quarter of them as a cubic on the FMA pipe, as in the bf16 forward, took 14 more instructions a pair
+// and was slower.
+__device__ __forceinline__ uint32_t exps(const uint32_t (&r)[32], uint32_t (&pk)[16], float (&acc)[4], float c, float nm) {
+  uint32_t top[2] = {0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    float x0, x1, p0, p1;
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
     fma2_bcast(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), c, nm);
-    if (!kMasked && (i & 3) == 3) {
-      exp2_fma_pair(p0, p1, x0, x1);
-    } else {
-      p0 = ex2_approx(x0);
-      p1 = ex2_approx(x1);
-    }
-    add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], p0, p1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    add2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], p0, p1);
     pk[i] = pack_f16x2(p0, p1);
+    asm("max.f16x2 %0, %0, %1;" : "+r"(top[i & 1]) : "r"(pk[i]));
   }
-  add2(acc[0], acc[1], acc[2], acc[3]);
-  add2(acc[4], acc[5], acc[6], acc[7]);
-  add2(acc[0], acc[1], acc[4], acc[5]);
-  return acc[0] + acc[1];
+  asm("max.f16x2 %0, %0, %1;" : "+r"(top[0]) : "r"(top[1]));
+  return max(top[0] & 0xFFFFu, top[0] >> 16);
+}
+constexpr uint32_t kTauF16 = 0x5C00u;  // 2^kTau
+
+// Q of a chunk of rows as the products take it: two tiles of 128 rows x D float16 as they lie in shared memory, then
+// [256] factors of the rows' scores, written ahead by kv4_chunk_q_kernel.  Request b's chunks start at q0 G / 256 + b,
+// so those of different requests do not meet.
+template <int D>
+constexpr size_t q_image_bytes() { return kRowsPerChunk * (D * 2 + 4); }
+template <int D>
+__device__ __forceinline__ uint8_t* q_image(const Kv4AttnParams& p, int b, int q0, int chunk, int h) {
+  const long long first = static_cast<long long>(q0) * p.G / kRowsPerChunk + b;
+  return p.ws_q + ((first + chunk) * p.Hk + h) * q_image_bytes<D>();
+}
+template <int D>
+__device__ __forceinline__ const float* q_factor(const Kv4AttnParams& p, const Segment& s) {
+  return reinterpret_cast<const float*>(q_image<D>(p, s.b, s.q0, s.chunk, s.h) + kRowsPerChunk * D * 2);
 }
 
-// A barrier of the four warps 8-11: whether all of them say yes.
+// One warp per row of a request (and key/value head): transformed in float32, scaled by a power of two that puts its
+// largest entry at 2^13 .. 2^14, rounded to float16.  Bound by memory (4 bytes per entry).  In the chunk kernel itself
+// this took 20,000 cycles per chunk in which the tensor core had nothing to do.
+constexpr int kQWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4AttnParams p) {
+  constexpr int E = D / 32;  // consecutive entries of a lane
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const SeqLen s = seq_len(p, b);
+  const int rows = s.nq * p.G, padded = (rows + kRowsPerChunk - 1) / kRowsPerChunk * kRowsPerChunk;
+  for (int row = blockIdx.x * kQWarps + (threadIdx.x >> 5); row < padded; row += gridDim.x * kQWarps) {
+    const int tok = row / p.G, hq = h * p.G + row - tok * p.G;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) w[e] = 0u;
+    if (row < rows) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (s.q0 + tok) * p.q_sn + hq * p.q_sh + E * lane;
+      if constexpr (E == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(src);
+      }
+    }
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+    if (p.signs != nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (p.signs[E * lane + e] == -1) x[e] = -x[e];
+#pragma unroll
+      for (int st = 1; st < E; st <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!(e & st)) {
+            const float u = x[e], v = x[e | st];
+            x[e] = u + v;
+            x[e | st] = u - v;
+          }
+#pragma unroll
+      for (int st = 1; st < 32; st <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float o = __shfl_xor_sync(0xffffffffu, x[e], st);
+          x[e] = (lane & st) ? o - x[e] : x[e] + o;
+        }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    const int ex = bits != 0u ? min(max(exponent_of(__uint_as_float(bits)) - 13, -100), 100) : 0;
+    const float f = exp2_int(-ex);
+    const int chunk = row / kRowsPerChunk, cr = row - chunk * kRowsPerChunk, tr = cr & 127;
+    uint8_t* image = q_image<D>(p, b, s.q0, chunk, h);
+    // entries 0 .. 7 of a 16-byte piece lie in 8 / E lanes; each stores its share of the pairs (0, 4) (1, 5) (2, 6) (3, 7)
+    uint8_t* at = image + (cr >> 7) * ChunkCfg<D>::kTileBytes + (lane * E / 64) * ChunkCfg<D>::kBoxBytes + tr * 128 +
+                  ((((lane * E / 8) & 7) ^ (tr & 7)) << 4);
+    if constexpr (E == 4) {
+      const bool up = lane & 1;  // entries 4 .. 7
+      const float s0 = __shfl_xor_sync(0xffffffffu, up ? x[0] : x[2], 1);
+      const float s1 = __shfl_xor_sync(0xffffffffu, up ? x[1] : x[3], 1);
+      *reinterpret_cast<uint2*>(at + (up ? 8 : 0)) = up ? make_uint2(pack_f16x2(s0 * f, x[2] * f), pack_f16x2(s1 * f, x[3] * f))
+                                                        : make_uint2(pack_f16x2(x[0] * f, s0 * f), pack_f16x2(x[1] * f, s1 * f));
+    } else {
+      const bool up = lane & 2;  // entries 4 .. 7; lane & 1: 2, 3 of the four
+      const float s0 = __shfl_xor_sync(0xffffffffu, up ? x[0] : x[1], 2);
+      *reinterpret_cast<uint32_t*>(at + ((lane & 1) ? 8 : 0) + (up ? 4 : 0)) =
+          up ? pack_f16x2(s0 * f, x[1] * f) : pack_f16x2(x[0] * f, s0 * f);
+    }
+    if (lane == 0)
+      reinterpret_cast<float*>(image + kRowsPerChunk * D * 2)[cr] = p.scale_log2 * exp2_int(ex);
+  }
+}
+
+// A barrier of warps 8-15: whether all of them say yes.
 __device__ __forceinline__ bool codes_all(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
   return r != 0;
 }
@@ -228,12 +317,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots];
-  __shared__ uint64_t kv_full[2], kv_empty[2], q_full[2], s_full[2], p_full[2], o_done[2], drained;
+  __shared__ uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drained;
   __shared__ uint32_t raw_gone[C::kRawSlots];
   __shared__ BlockInfo info[2];
-  __shared__ float wmax[2][2][4];
+  __shared__ float wmax[2][8];
+  __shared__ uint32_t wodd[2][4];
   __shared__ long long scan[C::kThreads / 32];
-  __shared__ ChunkWalk walks[14];
+  __shared__ ChunkWalk walks[18];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -241,12 +331,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   if (tid == 0) {
     for (int i = 0; i < C::kRawSlots; ++i) {
       bar_init(&raw_full[i], 1);
-      bar_init(&raw_empty[i], 4);
+      bar_init(&raw_empty[i], 8);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      bar_init(&kv_full[i], 8);
+      bar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&kv_full[i], 4);
-      bar_init(&kv_empty[i], 1);
-      bar_init(&q_full[i], 4);
+      bar_init(&q_full[i], 1);
+      bar_init(&q_empty[i], 1);
       bar_init(&s_full[i], 1);
       bar_init(&p_full[i], 4);
       bar_init(&o_done[i], 1);
@@ -298,7 +391,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       if (span0 < before + n) break;
       before += n;
     }
-    for (int w = 0; w < 14; ++w) {
+    for (int w = 0; w < 18; ++w) {
       walks[w].pos = span0;
       walks[w].end = span1;
       walks[w].first = before;
@@ -321,12 +414,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
 
   if (warp < 8) {
     // ================================================================ softmax, Q and O of tile q
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoftmax));
     const int q = warp >> 2;
     const int row = (warp & 3) * 32 + lane;  // of the tile, and lane of tensor memory
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tS = lane_base + q * 128, tO = lane_base + C::kOCol + q * D;
-    uint8_t* sq = smem + C::kQOff + q * C::kTileBytes;
     uint32_t blk = 0;   // blocks of keys so far
     uint32_t sit = 0;   // of them, blocks of this tile
     uint32_t uit = 0;   // segments of this tile
@@ -351,63 +442,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       const bool valid = q * 128 + row < rows;
       const int tok = rr / p.G, hq = S.h * p.G + rr - tok * p.G;
 
-      // Q: one row per thread, transformed in float32, largest entry at 2^13 .. 2^14
-      float c_row;
-      {
-        float x[D];
-        if (valid) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                            (S.q0 + tok) * p.q_sn + hq * p.q_sh);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 u = src[i];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-              x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D; ++i) x[i] = 0.f;
-        }
-        if (p.signs != nullptr) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const int4 sg = reinterpret_cast<const int4*>(p.signs)[i];
-            const int sw[4] = {sg.x, sg.y, sg.z, sg.w};
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (static_cast<signed char>(sw[k >> 2] >> (8 * (k & 3))) == -1) x[16 * i + k] = -x[16 * i + k];
-          }
-#pragma unroll
-          for (int st = 1; st < D; st <<= 1)
-#pragma unroll
-            for (int i = 0; i < D; ++i)
-              if (!(i & st)) {
-                const float a = x[i], b = x[i | st];
-                x[i] = a + b;
-                x[i | st] = a - b;
-              }
-        }
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < D; ++i) top = fmaxf(top, fabsf(x[i]));
-        const int ex = top > 0.f ? min(max(exponent_of(top) - 13, -100), 100) : 0;
-        const float f = exp2_int(-ex);
-        c_row = p.scale_log2 * exp2_int(ex);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const float* v = x + 8 * i;
-          *reinterpret_cast<uint4*>(sq + (i / 8) * C::kBoxBytes + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-              make_uint4(pack_f16x2(v[0] * f, v[4] * f), pack_f16x2(v[1] * f, v[5] * f), pack_f16x2(v[2] * f, v[6] * f),
-                         pack_f16x2(v[3] * f, v[7] * f));
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&q_full[q]);
+      const float c_row = q_factor<D>(p, S)[q * 128 + row];
 
       const int off = S.nk - S.nq;
       const int lim_row = !valid ? S.nk : p.causal ? min(S.nk, off + tok + 1) : S.nk;  // keys [0, lim_row) are seen
@@ -415,43 +450,73 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       float m = kNegBig, l = 0.f;
       int v_exp = 0;
       for (int t = S.t0; t < S.t1; ++t, ++blk, ++sit) {
-        ok = warp_all(wait_bar(&s_full[q], sit & 1u, ab));
+        // V of the block as well: its exponent goes into this block's P
+        const uint32_t v_item = 2 * blk + 1;
+        ok = warp_all(wait_bar(&s_full[q], sit & 1u, ab) &&
+                      wait_bar(&kv_full[v_item % C::kSlots], (v_item / C::kSlots) & 1u, ab));
         if (!ok) break;
         tc_fence_after();
-        const BlockInfo bi = info[blk & 1u];
+        const volatile BlockInfo& bi = info[blk & 1u];
         const float c = c_row * bi.k_back;
-        uint32_t r[128];
-        load_row(tS, r);
-        const int key0 = t * kBlockKeys;
-        const bool need_mask = key0 + kBlockKeys > lim_first || bi.gone != 0;
-        if (need_mask) {
-          const int lim = lim_row - key0;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim || ((bi.gone >> (i >> 4)) & 1u)) r[i] = __float_as_uint(-INFINITY);
-        }
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = __uint_as_float(r[i]);
-#pragma unroll
-        for (int i = 8; i < 128; i += 8)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(r[i + k]));
-        const float mb = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c;
+        const int lim = lim_row - t * kBlockKeys;
+        const uint32_t gone = bi.gone, odds = bi.odd[0] | bi.odd[1] | bi.odd[2] | bi.odd[3];
+        const bool need_mask = (t + 1) * kBlockKeys > lim_first || (gone | odds) != 0;
         float alpha = 1.f;
-        if (mb > m + kTau) {
-          alpha = ex2_approx(m - mb);
-          m = mb;
-          l *= alpha;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        // 32 keys at a time, p under the reference at hand; only where one comes out above 2^kTau the reference moves,
+        // and with it what was done under it.  P of 32 keys overwrites 16 columns of S that have been read.
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t r[32], pk[16];
+          tmem_ld_32cols(tS + 32 * k, r);
+          tmem_ld_wait(r);
+          if (need_mask) {
+            const uint32_t odd = bi.odd[k];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if ((odd >> i) & 1u) r[i] = 0x7FC00000u;  // a V that is not finite makes the rows that see it NaN
+              if (32 * k + i >= lim || ((gone >> (2 * k + (i >> 4))) & 1u)) r[i] = __float_as_uint(-INFINITY);
+            }
+          }
+          const float before[4] = {acc[0], acc[1], acc[2], acc[3]};
+          const uint32_t top = exps(r, pk, acc, c, -m);
+          if (__any_sync(0xffffffffu, top > kTauF16)) {
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
+#pragma unroll
+            for (int i = 4; i < 32; i += 4)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(r[i + j]));
+            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            float a = 1.f;
+            if (mb > m) {
+              a = ex2_approx(m - mb);
+              m = mb;
+            }
+            alpha *= a;
+            l *= a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = before[i] * a;
+            const uint32_t a2 = pack_f16x2(a, a);
+            tmem_st_wait();
+#pragma unroll 1
+            for (int j = 0; j < k; ++j) {
+              uint32_t old[16];
+              tmem_ld_16cols(tS + 16 * j, old);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(old[i]) : "r"(a2));
+              tmem_st_16cols(tS + 16 * j, old);
+            }
+            exps(r, pk, acc, c, -m);
+          }
+          tmem_st_16cols(tS + 16 * k, pk);
         }
-        uint32_t pk[64];
-        l += need_mask ? softmax_row<true>(r, pk, c, -m) : softmax_row<false>(r, pk, c, -m);
-        tmem_st_32cols(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st_32cols(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
         tmem_st_wait();
-        if (t > S.t0 && bi.v_exp != v_exp) alpha *= exp2_int(max(v_exp - bi.v_exp, -126));
-        v_exp = bi.v_exp;
+        const int ve = bi.v_exp;
+        if (t > S.t0 && ve != v_exp) alpha *= exp2_int(max(v_exp - ve, -126));
+        v_exp = ve;
         if (__any_sync(0xffffffffu, alpha != 1.f) && t > S.t0) {
           // O *= alpha: the P.V of the block before has completed (it was issued before this block's S)
           tc_fence_after();
@@ -516,139 +581,141 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       tc_fence_before();  // the next segment's first P.V comes after its q_full
     }
     if (tid == 0) *meta = found;
-  } else if (warp < 12) {
-    // ================================================================ codes to float16
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegCodes));
+  } else if (warp < 16) {
+    // ================================================================ codes to float16: K of a block, then its V
     const int ct = tid - 256;
-    const int c = ct & 3;
+    const int c = ct & 3, r = (ct >> 2) & 15, ti = (ct >> 6) & 1;  // keys 64 i + ct / 4, i = 0, 1
+    // where this thread's 16-byte pieces of its key 0 go; the second one of 8 dimensions is at ^ 16
+    const int put_at = (ct >> 2) * 128 + (((2 * c) ^ ((ct >> 2) & 7)) << 4);
     uint32_t blk = 0, pair = 0;
-    int v_exp = -200;  // reference exponent of V in this segment
     bool ok = true;
     Segment S;
     while (ok && take_segment(p, walks[warp], lane, S)) {
-      v_exp = -200;
-      for (int t = S.t0; t < S.t1 && ok; ++t, ++blk) {
+      int exp_v = -100;  // of V: the largest so far
+      for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += 4) {
+#pragma unroll 1
         for (int i = 0; i < 4 && ok; ++i)
           ok = warp_all(wait_bar(&raw_full[(pair + i) % C::kRawSlots], ((pair + i) / C::kRawSlots) & 1u, ab));
-        ok = ok && warp_all(wait_bar(&kv_empty[blk & 1u], ((blk >> 1) & 1u) ^ 1u, ab));
-        // largest values of the block, one key per thread; a key that is not there, or not finite, counts as zero
-        float mk = 0.f, mv = 0.f;
+        // the block's largest values: one key per thread, K's in the first four warps and V's in the others; a key that
+        // is not there, or not finite, counts as zero
+        float top = 0.f;
+        bool odd = false;
         if (ok) {
-          const uint32_t slot = (pair + (ct >> 5)) % C::kRawSlots;
-          const int ti = (ct >> 4) & 1, r = ct & 15;
-          const uint8_t* tile = smem + C::kRawOff + slot * C::kRawBytes + ti * F::kBytes;
-          if (!((raw_gone[slot] >> ti) & 1u) && t * kBlockKeys + ct < S.nk) {
+          const int key = ct & 127;
+          const uint32_t rs = (pair + (key >> 5)) % C::kRawSlots;
+          const int tj = (key >> 4) & 1;
+          const uint8_t* sz = smem + C::kRawOff + rs * C::kRawBytes + tj * F::kBytes + (warp >= 12 ? F::kVszOff : F::kKszOff) +
+                              (key & 15) * F::kSzRow;
+          if (!((raw_gone[rs] >> tj) & 1u) && t * kBlockKeys + key < S.nk) {
 #pragma unroll
             for (int g = 0; g < D / 64; ++g) {
-              const uint32_t k = *reinterpret_cast<const uint32_t*>(tile + F::kKszOff + r * F::kSzRow + 4 * g);
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + F::kVszOff + r * F::kSzRow + 4 * g);
-              const float ks = __uint_as_float(k << 16), kz = __uint_as_float(k & 0xFFFF0000u);
-              const float vs = __uint_as_float(v << 16), vz = __uint_as_float(v & 0xFFFF0000u);
-              mk = fmaxf(mk, fmaxf(fabsf(kz), fabsf(fmaf(15.f, ks, kz))));
-              mv = fmaxf(mv, fmaxf(fabsf(vz), fabsf(fmaf(15.f, vs, vz))));
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(sz + 4 * g);
+              const float step = __uint_as_float(w << 16), low = __uint_as_float(w & 0xFFFF0000u);
+              odd = odd || !(fabsf(low) < INFINITY && step < INFINITY);
+              top = fmaxf(top, fmaxf(fabsf(low), fabsf(fmaf(15.f, step, low))));
             }
           }
         }
-        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
-        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        const uint32_t odds = __ballot_sync(0xffffffffu, odd);
         if (lane == 0) {
-          wmax[blk & 1u][0][warp - 8] = mk;
-          wmax[blk & 1u][1][warp - 8] = mv;
+          wmax[blk & 1u][warp - 8] = top;
+          if (warp >= 12) wodd[blk & 1u][warp - 12] = odds;
         }
-        // the four warps meet here once per block, whatever came of their waits, and go on or stop together
+        // the eight warps meet here once per block, whatever came of their waits, and go on or stop together
         ok = codes_all(ok);
         if (!ok) break;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          mk = fmaxf(mk, wmax[blk & 1u][0][w]);
-          mv = fmaxf(mv, wmax[blk & 1u][1][w]);
-        }
-        // K's largest value of the block at 2^10 .. 2^11, V's of the segment so far at most there
-        const int ke = mk > 0.f ? min(max(exponent_of(mk) - 10, -110), 110) : 0;
-        const int ve = mv > 0.f ? min(max(exponent_of(mv) - 10, -110), 110) : -110;
-        v_exp = max(v_exp, ve);
-        const float kf = exp2_int(-ke), vf = exp2_int(-v_exp);
-        uint8_t* sk = smem + C::kKvOff + (blk & 1u) * 2 * C::kTileBytes;
-        uint8_t* sv = sk + C::kTileBytes;
-        uint32_t gone = 0;
+        const uint32_t gone01 = raw_gone[pair % C::kRawSlots] | (raw_gone[(pair + 1) % C::kRawSlots] << 2);
+        const uint32_t gone23 = raw_gone[(pair + 2) % C::kRawSlots] | (raw_gone[(pair + 3) % C::kRawSlots] << 2);
+        const uint32_t gone = gone01 | (gone23 << 4);
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t slot = (pair + i) % C::kRawSlots;
-          gone |= raw_gone[slot] << (2 * i);
-          const int key = 32 * i + (ct >> 2), ti = ct >> 6, r = (ct >> 2) & 15;
-          const uint8_t* tile = smem + C::kRawOff + slot * C::kRawBytes + ti * F::kBytes;
-          const bool there = !((raw_gone[slot] >> ti) & 1u) && t * kBlockKeys + key < S.nk;
-          uint32_t kw[2 * (D / 64)], vw[2 * (D / 64)];  // K: [group][8 dimensions]; V: [8 dimensions][group]
-          if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(tile + r * F::kRowBytes + 16 * c);
-            const uint4 b = *reinterpret_cast<const uint4*>(tile + F::kVOff + r * F::kRowBytes + 16 * c);
-            kw[0] = a.x, kw[1] = a.y, kw[2] = a.z, kw[3] = a.w;
-            vw[0] = b.x, vw[1] = b.y, vw[2] = b.z, vw[3] = b.w;
-          } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(tile + r * F::kRowBytes + 8 * c);
-            const uint2 b = *reinterpret_cast<const uint2*>(tile + F::kVOff + r * F::kRowBytes + 8 * c);
-            kw[0] = a.x, kw[1] = a.y;
-            vw[0] = b.x, vw[1] = b.y;
-          }
-          uint32_t ksz[D / 64], vsz[D / 64];
-          bool odd = false;  // a V that is not finite
+        for (int v = 0; v < 2 && ok; ++v) {
+          const uint32_t item = 2 * blk + v, slot = item % C::kSlots;
+          float most = 0.f;
 #pragma unroll
-          for (int g = 0; g < D / 64; ++g) {
-            ksz[g] = *reinterpret_cast<const uint32_t*>(tile + F::kKszOff + r * F::kSzRow + 4 * g);
-            vsz[g] = *reinterpret_cast<const uint32_t*>(tile + F::kVszOff + r * F::kSzRow + 4 * g);
-            if (!there) ksz[g] = vsz[g] = 0u;
-            const float vz = __uint_as_float(vsz[g] & 0xFFFF0000u);
-            odd = odd || !(fabsf(vz) < INFINITY) || !(__uint_as_float(vsz[g] << 16) < INFINITY);
-          }
+          for (int k = 0; k < 4; ++k) most = fmaxf(most, wmax[blk & 1u][4 * v + k]);
+          int e = most > 0.f ? min(max(exponent_of(most) + 8, -100), 110) : -100;
+          if (v) e = exp_v = max(exp_v, e);
+          const float f = exp2_int(-e);
+          const int codes_at = ti * F::kBytes + v * F::kVOff + r * F::kRowBytes + 8 * (D / 64) * c;
+          const int sz_at = ti * F::kBytes + (v ? F::kVszOff : F::kKszOff) + r * F::kSzRow;
+          ok = warp_all(wait_bar(&kv_empty[slot], ((item / C::kSlots) & 1u) ^ 1u, ab));
+          if (!ok) break;
+          uint8_t* to = smem + C::kKvOff + slot * C::kTileBytes;
 #pragma unroll
-          for (int g = 0; g < D / 64; ++g) {
-            // rows that do not see a key must not see its NaN either: V of such a key is zero, and its scores, which
-            // the mask replaces, are NaN
-            if (odd) ksz[g] = 0x7FC07FC0u, vsz[g] = 0u;
-            const float ks = __uint_as_float(ksz[g] << 16) * kf, kz = __uint_as_float(ksz[g] & 0xFFFF0000u) * kf;
-            const float vs = __uint_as_float(vsz[g] << 16) * vf, vz = __uint_as_float(vsz[g] & 0xFFFF0000u) * vf;
-            const uint32_t ks2 = pack_f16x2(ks, ks), kz2 = pack_f16x2(kz, kz);
-            const uint32_t vs2 = pack_f16x2(vs, vs), vz2 = pack_f16x2(vz, vz);
+          for (int i = 0; i < 2; ++i) {
+            const int key = 64 * i + (ct >> 2);
+            const uint8_t* raw = smem + C::kRawOff + ((pair + 2 * i + (ct >> 7)) % C::kRawSlots) * C::kRawBytes;
+            uint32_t w[2 * (D / 64)], sz[D / 64];  // [8 dimensions][group]
+            if constexpr (D == 128) {
+              const uint4 a = *reinterpret_cast<const uint4*>(raw + codes_at);
+              const uint2 b = *reinterpret_cast<const uint2*>(raw + sz_at);
+              w[0] = a.x, w[1] = v ? a.y : a.z, w[2] = v ? a.z : a.y, w[3] = a.w;
+              sz[0] = b.x, sz[1] = b.y;
+            } else {
+              const uint2 a = *reinterpret_cast<const uint2*>(raw + codes_at);
+              w[0] = a.x, w[1] = a.y;
+              sz[0] = *reinterpret_cast<const uint32_t*>(raw + sz_at);
+            }
+            // absent keys are zero; so is a V that is not finite (the rows that see it become NaN by its bit of odd;
+            // the others must not see it)
+            const bool zero = ((gone >> (key >> 4)) & 1u) || t * kBlockKeys + key >= S.nk ||
+                              (v && ((wodd[blk & 1u][key >> 5] >> (key & 31)) & 1u));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t at = g * C::kBoxBytes + key * 128 + (((2 * c + h) ^ (key & 7)) << 4);
-              *reinterpret_cast<uint4*>(sk + at) = expand(kw[2 * g + h], ks2, kz2);
-              *reinterpret_cast<uint4*>(sv + at) = expand(vw[(D / 64) * h + g], vs2, vz2);
+            for (int g = 0; g < D / 64; ++g) {
+              const Scales sc = scales_of(zero ? 0u : sz[g], f);
+              uint8_t* at = to + g * C::kBoxBytes + i * (64 * 128);
+              *reinterpret_cast<uint4*>(at + put_at) = expand(w[g], sc);
+              *reinterpret_cast<uint4*>(at + (put_at ^ 16)) = expand(w[(D / 64) + g], sc);
             }
           }
+          if (ct == 0) {
+            if (v) {
+              info[blk & 1u].v_exp = e;
+            } else {
+              info[blk & 1u].k_back = exp2_int(e);
+              info[blk & 1u].gone = gone;
+            }
+          }
+          if (v && ct < 4) info[blk & 1u].odd[ct] = wodd[blk & 1u][ct];
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) bar_arrive(&raw_empty[slot]);
+          if (lane == 0) bar_arrive(&kv_full[slot]);
         }
-        pair += 4;
-        if (ct == 0) info[blk & 1u] = BlockInfo{exp2_int(ke), v_exp, gone};
-        fence_proxy_async_smem();
+        if (lane < 4) bar_arrive(&raw_empty[(pair + lane) % C::kRawSlots]);
         __syncwarp();
-        if (lane == 0) bar_arrive(&kv_full[blk & 1u]);
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegOther));
-    if (warp == 12) {
+    if (warp == 16) {
       // ============================================================== MMA issuer
       constexpr uint32_t kIdS = make_idesc(128, 128, 0, false);  // float16, both K-major
       constexpr uint32_t kIdPV = make_idesc(128, D, 0, true);    // V MN-major
-      const uint32_t q_base = smem_addr(smem + C::kQOff), kv_base = smem_addr(smem + C::kKvOff);
-      uint32_t blk = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
-      auto issue_s = [&](int q, uint32_t buf) {
+      constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row atoms, version, 128-byte swizzle
+      const uint32_t q_lo = ((smem_addr(smem) + C::kQOff) >> 4) | (1u << 16);
+      const uint32_t kv_lo = (smem_addr(smem) + C::kKvOff) >> 4;
+      auto desc = [](uint32_t lo) {
+        uint64_t d;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(kDescHi));
+        return d;
+      };
+      uint32_t blk = 0, n_p = 0, n_q = 0;  // n_p, n_q: bit q is the parity of tile q's next phase
+      auto issue_s = [&](int q, uint32_t item) {
+        const uint32_t d = tmem + q * 128, a = q_lo + q * (C::kTileBytes >> 4);
+        const uint32_t b = (kv_lo + (item % C::kSlots) * (C::kTileBytes >> 4)) | (1u << 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * C::kBoxBytes + (kk % 4) * 32;
-          mma_f16_ss(tmem + q * 128, make_sdesc_sw128(q_base + q * C::kTileBytes + off, 16, 1024),
-                     make_sdesc_sw128(kv_base + buf * 2 * C::kTileBytes + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4;
+          mma_f16_ss(d, desc(a + off), desc(b + off), kIdS, kk > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[q]);
       };
-      auto issue_pv = [&](int q, uint32_t buf, bool acc) {
+      auto issue_pv = [&](int q, uint32_t item, bool acc) {
+        const uint32_t d = tmem + C::kOCol + q * D, a = tmem + q * 128;
+        const uint32_t b = (kv_lo + (item % C::kSlots) * (C::kTileBytes >> 4)) | (static_cast<uint32_t>(C::kBoxBytes >> 4) << 16);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + C::kOCol + q * D, tmem + q * 128 + kk * 8,
-                     make_sdesc_sw128(kv_base + (2 * buf + 1) * C::kTileBytes + kk * 16 * 128, C::kBoxBytes, 1024), kIdPV,
-                     (acc || kk > 0) ? 1u : 0u);
+          mma_f16_ts(d, a + kk * 8, desc(b + kk * (16 * 128 >> 4)), kIdPV, (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
       Segment S;
@@ -656,31 +723,38 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         const int tiles = min(ROWS, S.nq * p.G - S.chunk * ROWS) > 128 ? 2 : 1;
         if (lane == 0) {
           const int n = S.t1 - S.t0;
-          ok = wait_bar(&kv_full[blk & 1u], (blk >> 1) & 1u, ab);
-          for (int q = 0; q < tiles && ok; ++q) {
-            ok = wait_bar(&q_full[q], n_q[q]++ & 1u, ab);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(q, blk & 1u);
-          }
-          for (int j = 0; j < n && ok; ++j, ++blk) {
+          auto wait_item = [&](uint32_t item) { return wait_bar(&kv_full[item % C::kSlots], (item / C::kSlots) & 1u, ab); };
+          // turn j = -1 only brings in the first S; turn j: P.V of block j, then S of the next one, for each tile
+#pragma unroll 1
+          for (int j = -1; j < n && ok; ++j) {
+            const uint32_t k_item = 2 * blk + 2 * (j + 1), v_item = k_item - 1;  // of blocks j + 1 and j
             const bool more = j + 1 < n;
+            ok = (j < 0 || wait_item(v_item)) && (!more || wait_item(k_item));
+#pragma unroll 1
             for (int q = 0; q < tiles && ok; ++q) {
-              ok = wait_bar(&p_full[q], n_p[q]++ & 1u, ab);
+              if (j < 0) {
+                ok = wait_bar(&q_full[q], (n_q >> q) & 1u, ab);
+                n_q ^= 1u << q;
+              } else {
+                ok = wait_bar(&p_full[q], (n_p >> q) & 1u, ab);
+                n_p ^= 1u << q;
+              }
               if (!ok) break;
               tc_fence_after();
-              issue_pv(q, blk & 1u, j > 0);
-              if (q == tiles - 1) tc_commit(&kv_empty[blk & 1u]);
+              if (j >= 0) {
+                issue_pv(q, v_item, j > 0);
+                if (q == tiles - 1) tc_commit(&kv_empty[v_item % C::kSlots]);
+              }
               if (more) {
-                if (q == 0) ok = wait_bar(&kv_full[(blk + 1) & 1u], ((blk + 1) >> 1) & 1u, ab);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(q, (blk + 1) & 1u);
+                issue_s(q, k_item);
+                if (j + 2 == n) tc_commit(&q_empty[q]);
+                if (q == tiles - 1) tc_commit(&kv_empty[k_item % C::kSlots]);
               } else {
                 tc_commit(&o_done[q]);
               }
             }
           }
+          blk += n;
         }
         ok = warp_all(ok);
       }
@@ -689,12 +763,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         drain(&drained, 0);
       }
       __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
       // ============================================================== copies of the cache's tiles
-      uint32_t pair = 0;
+      uint32_t pair = 0, n_q[2] = {0, 0};
       bool ok = true;
       Segment S;
       while (ok && take_segment(p, walks[warp], lane, S)) {
+        // Q's tiles, once the products of the segment before have read theirs
+        const uint8_t* image = q_image<D>(p, S.b, S.q0, S.chunk, S.h);
+        const int tiles = min(ROWS, S.nq * p.G - S.chunk * ROWS) > 128 ? 2 : 1;
+        auto load_q = [&]() {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (q >= tiles || !ok) break;
+            ok = warp_all(wait_bar(&q_empty[q], (n_q[q] & 1u) ^ 1u, ab));
+            if (!ok) break;
+            ++n_q[q];
+            if (lane == 0) {
+              bar_arrive_expect_tx(&q_full[q], C::kTileBytes);
+              bulk_load_g2s(smem + C::kQOff + q * C::kTileBytes, image + q * C::kTileBytes, C::kTileBytes, &q_full[q]);
+            }
+            __syncwarp();
+          }
+        };
         const uint8_t* next = nullptr;
         int state = 0;  // of this lane's tile of the block: 0 past the keys, 1 there, 2 no block of the cache
         auto look = [&](int t) {
@@ -710,9 +801,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         };
         look(S.t0);
         for (int t = S.t0; t < S.t1 && ok; ++t) {
+          // after the first keys' copies: these run ahead into a new segment, its Q has to wait
+          if (t == S.t0 + 1 || S.t1 == S.t0 + 1) load_q();
           const uint8_t* src = next;
           const uint32_t there = __ballot_sync(0xffffffffu, state == 1), gone = __ballot_sync(0xffffffffu, state == 2);
           look(t + 1);  // one block ahead of its copies
+#pragma unroll 1
           for (int i = 0; i < 4 && ok; ++i, ++pair) {
             const uint32_t slot = pair % C::kRawSlots;
             ok = warp_all(wait_bar(&raw_empty[slot], ((pair / C::kRawSlots) & 1u) ^ 1u, ab));
@@ -729,9 +823,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         }
       }
       // after a wait that ran out, the copies in flight still land in this block's memory: wait for them
-      if (!ok && lane == 0)
+      if (!ok && lane == 0) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (n_q[q] > 0) drain(&q_full[q], (n_q[q] - 1) & 1u);
         for (uint32_t i = pair > C::kRawSlots ? pair - C::kRawSlots : 0; i < pair; ++i)
           drain(&raw_full[i % C::kRawSlots], (i / C::kRawSlots) & 1u);
+      }
       __syncwarp();
     }
   }
@@ -748,10 +846,18 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
 template <int D>
 cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   using C = ChunkCfg<D>;
-  kv4_chunk_kernel<D><<<num_sms, C::kThreads, C::kSmem, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  Kv4AttnParams q = p;
+  q.ws_q = p.ws + (part_bytes<D, kRowsPerChunk>(num_sms) + 255) / 256 * 256;
+  // a few rows per warp; requests shorter than the longest leave blocks without work
+  const long long rows = static_cast<long long>(p.max_q) * p.G;
+  const int per = static_cast<int>((rows + 4 * kQWarps - 1) / (4 * kQWarps));
+  kv4_chunk_q_kernel<D><<<dim3(per, p.Hk, p.B), kQWarps * 32, 0, stream>>>(q);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, kRowsPerChunk>(p, num_sms, 16, stream);
+  kv4_chunk_kernel<D><<<num_sms, C::kThreads, C::kSmem, stream>>>(q);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join<D, kRowsPerChunk>(q, num_sms, 16, stream);
 }
 
 }  // namespace
@@ -763,8 +869,11 @@ cudaError_t setup_kv4_chunk_kernels() {
   return e;
 }
 
-unsigned long long kv4_chunk_workspace_bytes(int d, int num_sms) {
-  return d == 64 ? part_bytes<64, kRowsPerChunk>(num_sms) : d == 128 ? part_bytes<128, kRowsPerChunk>(num_sms) : 0;
+unsigned long long kv4_chunk_workspace_bytes(int B, int Hk, int G, long long total_q, int d, int num_sms) {
+  // a request's chunks start anew: at most one more than its rows fill
+  const unsigned long long chunks = static_cast<unsigned long long>(total_q * G / kRowsPerChunk + B + 1) * Hk;
+  if (d == 64) return (part_bytes<64, kRowsPerChunk>(num_sms) + 255) / 256 * 256 + chunks * q_image_bytes<64>();
+  return (part_bytes<128, kRowsPerChunk>(num_sms) + 255) / 256 * 256 + chunks * q_image_bytes<128>();
 }
 
 cudaError_t launch_kv4_chunk(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream) {

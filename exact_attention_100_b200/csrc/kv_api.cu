@@ -199,13 +199,15 @@ int attn_kv4_read(const void* cache, const int* slots, void* k, void* v, int T, 
   return ATTN_OK;
 }
 
-unsigned long long attn_fwd_kv4_workspace_bytes(int d, int num_sms) {
-  if (!head_dim_ok(d) || num_sms < 0 || num_sms > 4096) return 0;
+unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total_q, int max_seqlen_q, int d, int num_sms) {
+  if (!head_dim_ok(d) || num_sms < 0 || num_sms > 4096 || B <= 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || total_q <= 0 ||
+      max_seqlen_q <= 0 || static_cast<long long>(total_q) * Hq > kIntMax || static_cast<long long>(B) * Hk > kIntMax)
+    return 0;
   if (num_sms == 0) {
     int* status = nullptr;
     if (ea::device_info(&num_sms, &status) != ATTN_OK) return 0;
   }
-  return ea::kv4_attn_workspace_bytes(d, num_sms);
+  return ea::kv4_attn_workspace_bytes(B, Hk, Hq / Hk, total_q, max_seqlen_q < total_q ? max_seqlen_q : total_q, d, num_sms);
 }
 
 int attn_fwd_kv4(const void* q, const void* cache, const int* block_table, const int* seq_lens,
@@ -220,7 +222,7 @@ int attn_fwd_kv4(const void* q, const void* cache, const int* block_table, const
   if (B <= 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || total_q <= 0 || max_seqlen_q <= 0 || width <= 0)
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(width) * page > kIntMax || static_cast<long long>(total_q) * Hq > kIntMax ||
-      static_cast<long long>(B) * Hk > kIntMax)
+      static_cast<long long>(B) * Hk > kIntMax || B > 65535 || Hk > 65535)
     return ATTN_ERR_INVALID_ARG;
   if (cu_seqlens_q == nullptr && (total_q != B || max_seqlen_q != 1)) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;

@@ -71,17 +71,19 @@ struct Kv4AttnParams {
   const signed char* signs;
   int* status;
   uint8_t* ws;
+  uint8_t* ws_q;             // set by launch_kv4_chunk: its Q, in the workspace
   long long q_sn, q_sh, o_sn, o_sh;
   int B, Hq, Hk, G, total_q, max_q, width, page, num_blocks;
   float scale_log2;          // softmax scale * log2 e (times 1 / sqrt d with the transform)
   int causal;
   int min_rows, max_rows;    // requests with min_rows < query length * G <= max_rows are this launch's
 };
-unsigned long long kv4_attn_workspace_bytes(int d, int num_sms);
+// Bytes for any lengths of B requests with total_q queries, none longer than max_q.
+unsigned long long kv4_attn_workspace_bytes(int B, int Hk, int G, long long total_q, int max_q, int d, int num_sms);
 cudaError_t setup_kv4_attn_kernels();
 // Requests of many rows (kv4_chunk.cu; d = 64, 128), called by launch_kv4_attn.
 cudaError_t setup_kv4_chunk_kernels();
-unsigned long long kv4_chunk_workspace_bytes(int d, int num_sms);
+unsigned long long kv4_chunk_workspace_bytes(int B, int Hk, int G, long long total_q, int d, int num_sms);
 cudaError_t launch_kv4_chunk(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches);
 

@@ -38,7 +38,7 @@ def declare(L) -> None:
     L.attn_kv4_append.restype = i
     L.attn_kv4_read.argtypes = [vp] * 4 + [i] * 6 + [vp]
     L.attn_kv4_read.restype = i
-    L.attn_fwd_kv4_workspace_bytes.argtypes = [i, i]
+    L.attn_fwd_kv4_workspace_bytes.argtypes = [i] * 7
     L.attn_fwd_kv4_workspace_bytes.restype = ctypes.c_ulonglong
     L.attn_fwd_kv4.argtypes = [vp] * 9 + [i] * 9 + [vp, f, i, vp]
     L.attn_fwd_kv4.restype = i
@@ -265,10 +265,11 @@ def attn_kv4_read(cache, slots, k=None, v=None, dtype=None):
     return k, v
 
 
-def attn_fwd_kv4_workspace_bytes(d, num_sms=0) -> int:
-    """Bytes of the workspace :func:`attn_fwd_kv4` needs on the current device (or on one of
-    ``num_sms`` processors)."""
-    return int(lib().attn_fwd_kv4_workspace_bytes(int(d), int(num_sms)))
+def attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, num_sms=0) -> int:
+    """Bytes of the workspace :func:`attn_fwd_kv4` needs for these arguments on the current device (or on
+    one of ``num_sms`` processors), whatever the requests' lengths."""
+    return int(lib().attn_fwd_kv4_workspace_bytes(int(B), int(Hq), int(Hk), int(total_q), int(max_seqlen_q), int(d),
+                                                  int(num_sms)))
 
 
 @_on_stream
@@ -311,7 +312,7 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
     if total_q == 0:
         return o, lse
     L = lib()
-    nbytes = L.attn_fwd_kv4_workspace_bytes(d, 0)
+    nbytes = L.attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, int(max_seqlen_q), d, 0)
     if workspace is None:
         workspace = q.new_empty(nbytes, dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:

@@ -122,11 +122,12 @@ int attn_kv4_read(const void* cache, const int* slots, void* k, void* v, int T, 
                   int num_blocks, int out_dtype, void* stream);
 
 /*
- * attn_fwd_kv4_workspace_bytes -- bytes of the workspace attn_fwd_kv4 needs (it depends on d and on the device's
- * processor count through num_sms, not on the lengths).  num_sms 0: of the current device.  0 for a d other
- * than 64, 128 or 256, or where there is no device to ask.
+ * attn_fwd_kv4_workspace_bytes -- bytes of the workspace attn_fwd_kv4 needs for these arguments, whatever the lengths of
+ * the requests are: partial results (20 to 40 MB), and where a request may have more than 32 rows per key/value head (at
+ * d = 64, 128) a float16 copy of Q.  num_sms 0: of the current device.  0 for arguments that attn_fwd_kv4 would refuse,
+ * or where there is no device to ask.
  */
-unsigned long long attn_fwd_kv4_workspace_bytes(int d, int num_sms);
+unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total_q, int max_seqlen_q, int d, int num_sms);
 
 /*
  * attn_fwd_kv4 -- attention of a packed batch of queries over the 4-bit cache, with grouped heads:
@@ -140,11 +141,11 @@ unsigned long long attn_fwd_kv4_workspace_bytes(int d, int num_sms);
  *   seq_lens    [B] int32: keys of request b, its new tokens among them; 0 .. width * page.
  *   cu_seqlens_q  [B + 1] int32 offsets of the requests' query rows, or NULL: one query per request
  *               (total_q = B).  Rows of q and o behind cu_seqlens_q[B] are not touched.
- *   max_seqlen_q  >= every query length (1 without cu_seqlens_q).
+ *   max_seqlen_q  >= every query length (1 without cu_seqlens_q).  B, Hk at most 65535.
  *   signs       as given to attn_kv4_append: Q is transformed alike.  NULL: none.
  *   causal      1: key j is visible to query i of a request iff j <= i + seq_len - query_len (the new
  *               tokens are the last ones); 0: every key.  A row with no key gets O = 0, LSE = -inf.
- *   workspace   attn_fwd_kv4_workspace_bytes(d, 0) bytes, 16-byte aligned, overwritten; not shared by calls
+ *   workspace   attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, 0) bytes, 16-byte aligned, overwritten; not shared by calls
  *               that may run at the same time.
  * Arithmetic: scores from exact products of the codes with Q in float16 (each row scaled by a power of two so
  * that its largest entry keeps all its bits; without the transform bf16 entries are exact over 2^-24 of it),

@@ -82,7 +82,8 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     V's step is rounded by 2^-11, which moves O by 2^-11 sum_j p_j (|v_j| + 15 s_j) <= 2^-11 3 sum_j p_j max|v_j| (a code
     times its step is at most the range, twice the largest value).
     Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18; the exponential of a quarter
-    of the keys is a cubic, off by 7.5e-5: x = 8e-5; V and p are rounded by 2^-11 each: 2^-10 sum_j p_j |v_j|.
+    of the keys is a cubic, off by 7.5e-5: x = 8e-5; V is rounded by 2^-11, p too, twice where the maximum moved:
+    3 2^-11 sum_j p_j |v_j|.
     O is rounded to bf16, 2^-8.  Second order: the whole times 1.1."""
     q = q.float().cpu().numpy().astype(np.float64)
     if signs is not None:
@@ -106,7 +107,7 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
                 p = np.exp(s - lse_ref[h, i])
                 dj = scale * e * (np.abs(k) @ np.abs(q[i, h])) + x * np.abs(s) + x
                 vmax = np.abs(v).max(-1, keepdims=True)
-                round_p = 2.0 ** -10 * (p @ np.abs(v)) if many else 2.0 ** -11 * 3 * (p @ vmax)
+                round_p = 3 * 2.0 ** -11 * (p @ np.abs(v)) if many else 2.0 ** -11 * 3 * (p @ vmax)
                 ob[i, h] = 1.1 * ((p * dj) @ np.abs(v - o_ref[i, h]) + round_p) + 2.0 ** -8 * np.abs(o_ref[i, h])
                 lb[h, i] = 1.1 * (p @ dj) + 2.0 ** -22 * (abs(lse_ref[h, i]) + 8)
     return ob, lb

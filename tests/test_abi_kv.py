@@ -91,8 +91,13 @@ def test_fwd_kv4_refusals(L):
                                (17, 1 << 26), (19, 0.0), (19, -1.0), (19, inf), (19, nan), (20, 2), (12, 1 << 27),
                                (4, NULL), (18, _arr(ctypes.c_longlong, 4096, 4, 4096, 128))], BAD)
     _each(L.attn_fwd_kv4, ok, [(14, 96), (14, 32)], UNSUP)
-    assert L.attn_fwd_kv4_workspace_bytes(96, 148) == 0 and L.attn_fwd_kv4_workspace_bytes(128, -1) == 0
-    assert L.attn_fwd_kv4_workspace_bytes(128, 148) > 0
+    w = L.attn_fwd_kv4_workspace_bytes
+    good = [4, 32, 8, 40, 16, 128, 148]
+    assert w(*good) > 0
+    for idx, val in [(0, 0), (1, 0), (1, 30), (2, 0), (3, 0), (4, 0), (5, 96), (6, -1), (3, 1 << 27)]:
+        a = list(good)
+        a[idx] = val
+        assert w(*a) == 0, (idx, val)
 
 
 def test_binding_refuses_before_any_library_call(L):
