@@ -24,27 +24,31 @@ namespace {
 constexpr int kHeads = 4;
 constexpr int kThreads = 256;
 
-template <int VEC>
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[VEC]) {
-  uint32_t w[VEC / 2];
-  if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x, w[1] = u.y;
+// VEC values as they lie in memory (kept so until they are used: half the registers of their floats), and as floats
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int kWords = VEC * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
   }
-}
+};
+
 template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
+__device__ __forceinline__ void load_table(const float* p, float (&v)[VEC]) {
 #pragma unroll
   for (int i = 0; i < VEC; i += 4) {
-    const float4 u = *reinterpret_cast<const float4*>(p + i);
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p + i));
     v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
   }
 }
@@ -65,21 +69,23 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
 
 // Work is numbered ((token * chunks + head chunk) * lanes + lane): lanes 0 .. half / VEC - 1 rotate VEC
 // pairs each, the lanes behind them copy VEC of the coordinates past 2 * half (none if 2 * half = d).
-template <typename TI, typename TO, int VEC>
+// I numbers the work: 32 bits wherever it has fewer than 2^31 pieces (three divisions of 64 bits per piece took as
+// long as the memory: 54 us for 8,192 tokens of 40 heads of 128).
+template <typename TI, typename TO, int VEC, typename I>
 __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeParams p) {
   const int rot_lanes = p.half / VEC;
   const int lanes = rot_lanes + (p.d - 2 * p.half) / VEC;
   const int heads = p.H[0] + p.H[1];
   const int chunks = (heads + kHeads - 1) / kHeads;
   const long long tokens = static_cast<long long>(p.B) * p.N;
-  const long long total = tokens * chunks * lanes;
-  const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; id < total; id += step) {
-    const int lane = static_cast<int>(id % lanes);
-    const long long rest = id / lanes;
-    const int h0 = static_cast<int>(rest % chunks) * kHeads;
-    const long long tok = rest / chunks;
-    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
+  const I total = static_cast<I>(tokens) * chunks * lanes;
+  const I step = static_cast<I>(gridDim.x) * kThreads;
+  for (I id = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x; id < total; id += step) {
+    const I rest = id / lanes;
+    const int lane = static_cast<int>(id - rest * lanes);
+    const I tok = rest / chunks;
+    const int h0 = static_cast<int>(rest - tok * chunks) * kHeads;
+    const int b = p.B == 1 ? 0 : static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<I>(b) * p.N);
     const bool rot = lane < rot_lanes;
     float c[VEC], s[VEC];
     bool ok[VEC];
@@ -92,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeParams p)
       if (i0 + VEC <= p.sec_end[ax0]) {  // all VEC pairs turn with one axis
         all = pos0 >= 0 && pos0 < p.n_pos;
         const long long at = static_cast<long long>(all ? pos0 : 0) * p.half + i0;
-        load_vec<VEC>(p.cos + at, c);
-        load_vec<VEC>(p.sin + at, s);
+        load_table<VEC>(p.cos + at, c);
+        load_table<VEC>(p.sin + at, s);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) ok[i] = all;
       } else {
@@ -118,15 +124,15 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeParams p)
     // first and second coordinate of the lane's vectors (a copying lane has one)
     const int ca = rot ? lane * VEC : 2 * p.half + (lane - rot_lanes) * VEC;
     const int cb = rot ? p.half + lane * VEC : ca;
-    float a[kHeads][VEC], d[kHeads][VEC];
+    Raw<TI, VEC> a[kHeads], d[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j;
       if (h < heads) {
         const int t = h < p.H[0] ? 0 : 1;
         const TI* x = static_cast<const TI*>(p.x[t]) + b * p.xs[t][0] + (t ? h - p.H[0] : h) * p.xs[t][1] + n * p.xs[t][2];
-        load_vec<VEC>(x + ca, a[j]);
-        if (rot) load_vec<VEC>(x + cb, d[j]);
+        a[j].load(x + ca);
+        if (rot) d[j].load(x + cb);
       }
     }
 #pragma unroll
@@ -136,14 +142,18 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeParams p)
         const int t = h < p.H[0] ? 0 : 1;
         TO* y = static_cast<TO*>(p.y[t]) + b * p.ys[t][0] + (t ? h - p.H[0] : h) * p.ys[t][1] + n * p.ys[t][2];
         if (!rot) {
-          store_vec<VEC>(y + ca, a[j]);
+          float u[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) u[i] = a[j].at(i);
+          store_vec<VEC>(y + ca, u);
           continue;
         }
         float u[VEC], v[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          u[i] = __fsub_rn(__fmul_rn(a[j][i], c[i]), __fmul_rn(d[j][i], s[i]));
-          v[i] = __fadd_rn(__fmul_rn(d[j][i], c[i]), __fmul_rn(a[j][i], s[i]));
+          const float xa = a[j].at(i), xb = d[j].at(i);
+          u[i] = __fsub_rn(__fmul_rn(xa, c[i]), __fmul_rn(xb, s[i]));
+          v[i] = __fadd_rn(__fmul_rn(xb, c[i]), __fmul_rn(xa, s[i]));
         }
         if (all) {
           store_vec<VEC>(y + ca, u);
@@ -168,7 +178,10 @@ cudaError_t launch(const RopeParams& p, int num_sms, cudaStream_t stream) {
   const long long total = static_cast<long long>(p.B) * p.N * chunks * lanes;
   const long long want = (total + kThreads - 1) / kThreads;
   const long long cap = static_cast<long long>(num_sms) * 32;
-  rope_axes_kernel<TI, TO, VEC><<<static_cast<int>(want < cap ? want : cap), kThreads, 0, stream>>>(p);
+  const int grid = static_cast<int>(want < cap ? want : cap);
+  // below 2^31 pieces plus a round of the grid, the unsigned counter does not wrap
+  if (total < (1ll << 31)) rope_axes_kernel<TI, TO, VEC, unsigned><<<grid, kThreads, 0, stream>>>(p);
+  else rope_axes_kernel<TI, TO, VEC, unsigned long long><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
