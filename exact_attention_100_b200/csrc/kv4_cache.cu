@@ -9,7 +9,11 @@
 // Bound by memory: 4 bytes of K and V read and 1.125 written per value pair.  A lane holds 16
 // consecutive values of a row (two 16-byte loads, d / 16 lanes per row, several rows per warp), so four of
 // the transform's stages and most of the minimum and maximum stay in the lane, and a group is four
-// adjacent lanes.  K and V rows go to different blocks of threads.
+// adjacent lanes.  K and V rows go to different blocks of threads.  The quotients come from the group's one
+// reciprocal, corrected to the rounded quotient (three operations instead of a division each: 54 us before for
+// 16,384 tokens of 8 heads of 128).
+//
+// Read: a thread has four dimensions of a row, so that each store of a warp is contiguous.
 
 #include <cuda_bf16.h>
 
@@ -33,6 +37,18 @@ __device__ __forceinline__ float bf16_up(float x) {  // x >= 0
   return __uint_as_float((__float_as_uint(x) + 0xFFFFu) & 0xFFFF0000u);
 }
 
+// minimum and maximum that a NaN goes through
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CacheParams p) {
   using F = Kv4Tile<D>;
@@ -41,13 +57,12 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CachePara
   const int j = lane % kLanes;
   const bool is_v = blockIdx.y != 0;
   const bool transform = !is_v && p.signs != nullptr;
-  const long long rows = static_cast<long long>(p.T) * p.Hk;
-  const long long row = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-  const bool live = row < rows;
+  // fewer than 2^31 rows (the caller's bound), and a block of threads past them at most
+  const unsigned row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   int t = 0, h = 0, slot = -1;
-  if (live) {
-    t = static_cast<int>(row / p.Hk);
-    h = static_cast<int>(row - static_cast<long long>(t) * p.Hk);
+  if (row < static_cast<unsigned>(p.T) * static_cast<unsigned>(p.Hk)) {
+    t = static_cast<int>(row / static_cast<unsigned>(p.Hk));
+    h = static_cast<int>(row) - t * p.Hk;
     slot = p.slots[t];
   }
   float x[16];
@@ -81,43 +96,58 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CachePara
         }
 #pragma unroll
     for (int s = 1; s < kLanes; s <<= 1) {
-      const bool hi = (j & s) != 0;
+      const float sign = (j & s) ? -1.f : 1.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float o = __shfl_xor_sync(0xffffffffu, x[i], s);
-        x[i] = hi ? o - x[i] : x[i] + o;
-      }
+      for (int i = 0; i < 16; ++i)  // other + x, or other - x: the product is exact
+        x[i] = fmaf(sign, x[i], __shfl_xor_sync(0xffffffffu, x[i], s));
     }
     constexpr float kNorm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], kNorm);
   }
   float lo = x[0], hi = x[0];
-  bool odd = false;  // a value that is not finite
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = odd || !isfinite(x[i]);
+  for (int i = 1; i < 16; ++i) {
+    lo = min_nan(lo, x[i]);
+    hi = max_nan(hi, x[i]);
   }
 #pragma unroll
   for (int s = 1; s < 4; s <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
   }
   float z = bf16_down(lo);
   const float range = __fsub_rn(hi, z);
-  const unsigned odds = __ballot_sync(0xffffffffu, odd || !isfinite(range));
+  // a NaN goes through the minimum and the maximum, an infinity makes the range infinite or NaN
+  const unsigned odds = __ballot_sync(0xffffffffu, !isfinite(range));
   float s = bf16_up(__fdiv_rn(range, 15.f));
   uint32_t code[2] = {0u, 0u};
   if ((odds >> (lane & ~3)) & 15u) {
     s = z = __uint_as_float(0x7FC00000u);
-  } else if (s > 0.f) {
+  } else if (s > 1e-30f && s < 1e30f) {
+    // With y = 1 / s rounded, q = t y and the exact remainder t - q s, q + remainder y is the rounded quotient (Markstein).
+    // It is at least 0 and rounds to 15 at most; 1.5 2^23 added rounds it to the nearest integer, in the low bits.
+    const float y = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], z), s)), 0.f), 15.f);
-      code[i >> 3] |= static_cast<uint32_t>(u) << (4 * (i & 7));
+    for (int w = 0; w < 2; ++w) {
+      uint32_t c = 0u;
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        const float u = __fsub_rn(x[8 * w + i], z);
+        const float q = __fmul_rn(u, y);
+        const float n = __fadd_rn(fmaf(fmaf(-q, s, u), y, q), 12582912.f);
+        c = c * 16u + __float_as_uint(n);
+      }
+      code[w] = c - 0x11111111u * 0x4B400000u;  // what the shift's own bits add up to
     }
+  } else if (s > 0.f) {
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(w ? x[8 + i] : x[i], z), s)), 0.f), 15.f);
+        code[w] |= static_cast<uint32_t>(u) << (4 * i);
+      }
   }
   if (slot == -1) return;
   const int block = slot / p.page, off = slot - block * p.page;
@@ -141,67 +171,87 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CachePara
         (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xFFFF0000u);
 }
 
+// One store of a warp: half a row of d = 256, a row of 128, two of 64.  A warp has kReadRows such rows (or pairs), whose
+// loads are in flight together; each of its lanes finds one of them in the cache (every lane for itself, the divisions
+// took longer than the memory).
+constexpr int kReadRows = 8;
+
+template <int D>
+struct ReadCfg {
+  static constexpr int kLanes = D / 4;                              // of a row, four dimensions each
+  static constexpr int kAtOnce = kLanes < 32 ? 32 / kLanes : 1;     // rows of one store
+  static constexpr int kWarpsPerRow = kLanes > 32 ? kLanes / 32 : 1;
+  static constexpr int kRowsPerWarp = kAtOnce * kReadRows;
+  static constexpr int kRowsPerBlock = kThreads / 32 / kWarpsPerRow * kRowsPerWarp;
+};
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4CacheParams p) {
   using F = Kv4Tile<D>;
-  constexpr int kLanes = D / 16;
-  const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const int j = static_cast<int>(id % kLanes);
-  const long long row = id / kLanes;
-  if (row >= static_cast<long long>(p.T) * p.Hk) return;
+  using C = ReadCfg<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = 4 * (threadIdx.x % C::kLanes);  // this thread's dimensions x .. x + 3
   const bool is_v = blockIdx.y != 0;
-  const int t = static_cast<int>(row / p.Hk), h = static_cast<int>(row - static_cast<long long>(t) * p.Hk);
-  const int slot = p.slots[t];
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  const int block = slot < 0 ? 0 : slot / p.page, off = slot - block * p.page;
-  if (slot < -1 || block >= p.num_blocks) atomicOr(p.status, kDevStatusBadSeqlens);
-  if (slot >= 0 && block < p.num_blocks) {
-    const uint8_t* tile = p.cache + kv4_tile_offset<D>(block, off, p.page, p.Hk, h);
-    const int r = off & 15;
-    const int plane = j / (F::kPlaneDims / 16), g = (j / 4) % F::kGroups, c = j & 3;
-    uint32_t code[2];
-    if (!is_v) {
-      const uint2 w = *reinterpret_cast<const uint2*>(tile + plane * F::kPlaneBytes + r * F::kRowBytes +
-                                                      c * 8 * F::kGroups + 8 * g);
-      code[0] = w.x, code[1] = w.y;
-    } else {
-      const uint8_t* d = tile + F::kVOff + plane * F::kPlaneBytes + r * F::kRowBytes + 2 * c * 4 * F::kGroups + 4 * g;
-      code[0] = *reinterpret_cast<const uint32_t*>(d);
-      code[1] = *reinterpret_cast<const uint32_t*>(d + 4 * F::kGroups);
-    }
-    const uint32_t sz = *reinterpret_cast<const uint32_t*>(tile + (is_v ? F::kVszOff : F::kKszOff) + r * F::kSzRow +
-                                                           4 * (j / 4));
-    const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xFFFF0000u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = fmaf(static_cast<float>((code[i >> 3] >> (4 * (i & 7))) & 15u), s, z);
+  const int xp = x % F::kPlaneDims, g = xp / 64, rr = xp % 64;
+  const int code_at = (is_v ? F::kVOff + (rr / 8) * 4 * F::kGroups + 4 * g + (rr % 8) / 2
+                            : (rr / 16) * 8 * F::kGroups + 8 * g + (rr % 16) / 2) + (x / F::kPlaneDims) * F::kPlaneBytes;
+  const int sz_at = (is_v ? F::kVszOff : F::kKszOff) + 4 * (x / 64);
+  const unsigned rows = static_cast<unsigned>(p.T) * static_cast<unsigned>(p.Hk);
+  const unsigned first = blockIdx.x * C::kRowsPerBlock + (warp / C::kWarpsPerRow) * C::kRowsPerWarp;
+  // lane i: where row first + i lies, its row in the tile in the upper 8 bits; all ones: nowhere
+  unsigned long long at = ~0ull;
+  if (lane < C::kRowsPerWarp && first + lane < rows) {
+    const unsigned row = first + lane;
+    const int t = static_cast<int>(row / static_cast<unsigned>(p.Hk)), h = static_cast<int>(row) - t * p.Hk;
+    const int slot = p.slots[t];
+    const int block = slot < 0 ? 0 : slot / p.page, off = slot - block * p.page;
+    if (slot < -1 || block >= p.num_blocks) atomicOr(p.status, kDevStatusBadSeqlens);
+    else if (slot >= 0)
+      at = static_cast<unsigned long long>(kv4_tile_offset<D>(block, off, p.page, p.Hk, h)) |
+           (static_cast<unsigned long long>(off & 15) << 56);
   }
-  const long long at = row * D + 16 * j;
-  if constexpr (F32) {
-    float4* out = reinterpret_cast<float4*>(static_cast<float*>(is_v ? p.v_out : p.k_out) + at);
+  const int sub = lane / C::kLanes;  // 0, or which of two rows
+  uint32_t code[kReadRows], sz[kReadRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  } else {
-    uint32_t w[8];
+  for (int i = 0; i < kReadRows; ++i) {
+    const unsigned long long a = __shfl_sync(0xffffffffu, at, i * C::kAtOnce + sub);
+    code[i] = sz[i] = 0u;
+    if (a != ~0ull) {
+      const uint8_t* tile = p.cache + (a & ((1ull << 56) - 1));
+      const int r = static_cast<int>(a >> 56);
+      code[i] = *reinterpret_cast<const uint16_t*>(tile + code_at + r * F::kRowBytes);
+      sz[i] = *reinterpret_cast<const uint32_t*>(tile + sz_at + r * F::kSzRow);
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_out : p.k_out) + at);
-    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int i = 0; i < kReadRows; ++i) {
+    const unsigned row = first + i * C::kAtOnce + sub;
+    if (row >= rows) break;
+    const float s = __uint_as_float(sz[i] << 16), z = __uint_as_float(sz[i] & 0xFFFF0000u);
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(static_cast<float>((code[i] >> (4 * k)) & 15u), s, z);
+    const long long to = static_cast<long long>(row) * D + x;
+    if constexpr (F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(is_v ? p.v_out : p.k_out) + to) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(v[2 * k + 1]), "f"(v[2 * k]));
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(is_v ? p.v_out : p.k_out) + to) = make_uint2(w[0], w[1]);
+    }
   }
 }
 
-dim3 grid_of(const Kv4CacheParams& p, int d) {
-  const long long threads = static_cast<long long>(p.T) * p.Hk * (d / 16);
-  return dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads), 2);
+dim3 grid_of(const Kv4CacheParams& p, int rows_per_block) {
+  const long long rows = static_cast<long long>(p.T) * p.Hk;
+  return dim3(static_cast<unsigned>((rows + rows_per_block - 1) / rows_per_block), 2);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4CacheParams& p, int d, cudaStream_t stream) {
-  const dim3 grid = grid_of(p, d);
+  const dim3 grid = grid_of(p, kThreads / (d / 16));
   if (d == 64) kv4_append_kernel<64><<<grid, kThreads, 0, stream>>>(p);
   else if (d == 128) kv4_append_kernel<128><<<grid, kThreads, 0, stream>>>(p);
   else kv4_append_kernel<256><<<grid, kThreads, 0, stream>>>(p);
@@ -209,7 +259,8 @@ cudaError_t launch_kv4_append(const Kv4CacheParams& p, int d, cudaStream_t strea
 }
 
 cudaError_t launch_kv4_read(const Kv4CacheParams& p, int d, bool out_f32, cudaStream_t stream) {
-  const dim3 grid = grid_of(p, d);
+  const dim3 grid = grid_of(p, d == 64 ? ReadCfg<64>::kRowsPerBlock : d == 128 ? ReadCfg<128>::kRowsPerBlock
+                                                                              : ReadCfg<256>::kRowsPerBlock);
   if (out_f32) {
     if (d == 64) kv4_read_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
     else if (d == 128) kv4_read_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
