@@ -117,18 +117,21 @@ def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, 
            _arg(cursor, (1,), i32, "cursor", dev))
     if slots is None and positions is None and cu_seqlens is None and lens_out is None and cursor_out is None:
         # one allocation for the five
-        slots, positions, cu_seqlens, lens_out, cursor_out = lens.new_empty(2 * total + 2 * B + 2).split(
-            (total, total, B + 1, B, 1))
-    slots = slots if slots is not None else lens.new_empty(total)
-    positions = positions if positions is not None else lens.new_empty(total)
-    cu_seqlens = cu_seqlens if cu_seqlens is not None else lens.new_empty(B + 1)
-    lens_out = lens_out if lens_out is not None else lens.new_empty(B)
-    cursor_out = cursor_out if cursor_out is not None else lens.new_empty(1)
-    _check(lib().attn_kv_tables(*ins, _arg(slots, (total,), i32, "slots", dev),
-                                _arg(positions, (total,), i32, "positions", dev),
-                                _arg(cu_seqlens, (B + 1,), i32, "cu_seqlens", dev),
-                                _arg(lens_out, (B,), i32, "lens_out", dev), _arg(cursor_out, (1,), i32, "cursor_out", dev),
-                                B, width, int(page_size), n_free, total, _raw_stream(torch, dev)), "attn_kv_tables")
+        room = lens.new_empty(2 * total + 2 * B + 2)
+        slots, positions, cu_seqlens, lens_out, cursor_out = room.split((total, total, B + 1, B, 1))
+        at = room.data_ptr()
+        outs = (at, at + 4 * total, at + 8 * total, at + 8 * total + 4 * B + 4, at + 8 * total + 8 * B + 4)
+    else:
+        slots = slots if slots is not None else lens.new_empty(total)
+        positions = positions if positions is not None else lens.new_empty(total)
+        cu_seqlens = cu_seqlens if cu_seqlens is not None else lens.new_empty(B + 1)
+        lens_out = lens_out if lens_out is not None else lens.new_empty(B)
+        cursor_out = cursor_out if cursor_out is not None else lens.new_empty(1)
+        outs = (_arg(slots, (total,), i32, "slots", dev), _arg(positions, (total,), i32, "positions", dev),
+                _arg(cu_seqlens, (B + 1,), i32, "cu_seqlens", dev), _arg(lens_out, (B,), i32, "lens_out", dev),
+                _arg(cursor_out, (1,), i32, "cursor_out", dev))
+    _check(lib().attn_kv_tables(*ins, *outs, B, width, int(page_size), n_free, total, _raw_stream(torch, dev)),
+           "attn_kv_tables")
     return slots, positions, cu_seqlens, lens_out, cursor_out, block_table
 
 
@@ -156,8 +159,9 @@ def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse,
     if positions.dim() == 1 and q.dim() == 3 and len(sections) == 1:
         positions = positions[None]
     at = _arg(positions, (len(sections), N) if q.dim() == 3 else (len(sections), B, N), torch.int32, "positions", dev)
+    out_dtype = out_dtype or (q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else q.dtype)
     if q_out is None:
-        q_out = torch.empty_like(q, dtype=out_dtype or q.dtype)
+        q_out = torch.empty_like(q, dtype=out_dtype)
     pqo = _rows(q_out, q.shape, types, "q_out", dev)
     strides_k = strides_ko = (8, 8, 8)
     Hk = pk = pko = 0
@@ -256,9 +260,16 @@ def attn_kv4_read(cache, slots, k=None, v=None, dtype=None):
     dt = dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
     if dt not in (torch.bfloat16, torch.float32):
         raise ValueError("the values are bf16 or float32")
-    k = k if k is not None else cache.new_empty((T, Hk, d), dtype=dt)
-    v = v if v is not None else cache.new_empty((T, Hk, d), dtype=dt)
-    pk, pv = _arg(k, (T, Hk, d), dt, "k", dev), _arg(v, (T, Hk, d), dt, "v", dev)
+    if k is None:
+        k = cache.new_empty((T, Hk, d), dtype=dt)
+        pk = k.data_ptr()
+    else:
+        pk = _arg(k, (T, Hk, d), dt, "k", dev)
+    if v is None:
+        v = cache.new_empty((T, Hk, d), dtype=dt)
+        pv = v.data_ptr()
+    else:
+        pv = _arg(v, (T, Hk, d), dt, "v", dev)
     if T:
         _check(lib().attn_kv4_read(pc, ps, pk, pv, T, Hk, d, page, nb, ATTN_FP32 if dt is torch.float32 else ATTN_BF16,
                                    _raw_stream(torch, dev)), "attn_kv4_read")
@@ -270,6 +281,10 @@ def attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, num_sms=0)
     one of ``num_sms`` processors), whatever the requests' lengths."""
     return int(lib().attn_fwd_kv4_workspace_bytes(int(B), int(Hq), int(Hk), int(total_q), int(max_seqlen_q), int(d),
                                                   int(num_sms)))
+
+
+# bytes of the workspace by (B, Hq, Hk, total_q, max_seqlen_q, d, device): asking takes as long as a tensor
+_workspace_bytes = {}
 
 
 @_on_stream
@@ -305,20 +320,32 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
     pg = _sign_arg(signs, d, torch, dev)
     if o is None:
         o = q.new_empty((total_q, Hq, d))
-    po = _rows(o, (total_q, Hq, d), bf16, "o", dev)
-    if lse is None and want_lse:
+        po, so = o.data_ptr(), (Hq * d, d)
+    else:
+        po, so = _rows(o, (total_q, Hq, d), bf16, "o", dev), o.stride()[:2]
+    pe = 0
+    if lse is not None:
+        pe = _arg(lse, (Hq, total_q), torch.float32, "lse", dev)
+    elif want_lse:
         lse = q.new_empty((Hq, total_q), dtype=torch.float32)
-    pe = _arg(lse, (Hq, total_q), torch.float32, "lse", dev) if lse is not None else 0
+        pe = lse.data_ptr()
     if total_q == 0:
         return o, lse
-    L = lib()
-    nbytes = L.attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, int(max_seqlen_q), d, 0)
+    L, max_seqlen_q = lib(), int(max_seqlen_q)
+    sizes = (B, Hq, Hk, total_q, max_seqlen_q, d, dev)
+    nbytes = _workspace_bytes.get(sizes)
+    if nbytes is None:
+        if len(_workspace_bytes) >= 4096:
+            _workspace_bytes.clear()
+        nbytes = _workspace_bytes[sizes] = L.attn_fwd_kv4_workspace_bytes(*sizes[:6], 0)
     if workspace is None:
         workspace = q.new_empty(nbytes, dtype=torch.uint8)
-    elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"attn_fwd_kv4: the workspace must be contiguous and have {nbytes} bytes")
-    pw = _arg(workspace, workspace.shape, workspace.dtype, "workspace", dev)
-    _check(L.attn_fwd_kv4(pq, pc, pt, pl, pcu, po, pe, pw, pg, B, Hq, Hk, total_q, int(max_seqlen_q), d, page, nb, width,
-                          _LL4(*q.stride()[:2], *o.stride()[:2]), float(scale) if scale is not None else 1.0 / math.sqrt(d),
+        pw = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError(f"attn_fwd_kv4: the workspace must be contiguous and have {nbytes} bytes")
+        pw = _arg(workspace, workspace.shape, workspace.dtype, "workspace", dev)
+    _check(L.attn_fwd_kv4(pq, pc, pt, pl, pcu, po, pe, pw, pg, B, Hq, Hk, total_q, max_seqlen_q, d, page, nb, width,
+                          _LL4(*q.stride()[:2], *so), float(scale) if scale is not None else 1.0 / math.sqrt(d),
                           1 if causal else 0, _raw_stream(torch, dev)), "attn_fwd_kv4")
     return o, lse
