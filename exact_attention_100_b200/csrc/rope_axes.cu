@@ -72,7 +72,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
 // I numbers the work: 32 bits wherever it has fewer than 2^31 pieces (three divisions of 64 bits per piece took as
 // long as the memory: 54 us for 8,192 tokens of 40 heads of 128).
 template <typename TI, typename TO, int VEC, typename I>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const RopeParams p) {
   const int rot_lanes = p.half / VEC;
   const int lanes = rot_lanes + (p.d - 2 * p.half) / VEC;
   const int heads = p.H[0] + p.H[1];
