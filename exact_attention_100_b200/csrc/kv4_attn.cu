@@ -7,13 +7,13 @@
 // so the tensor core multiplies the codes themselves, and steps and minima meet them in the small
 // products: once per (key, row, group) instead of once per element.
 //
-// Bound by memory: 1.125 d bytes per key and key/value head for at least 4 d G flops.  The arithmetic has to
-// stay under the time the bytes take, about 100 cycles of an SM per 16 keys at d = 128; rows of q are few,
-// so the products are the warp's m16n8k16 with keys (then dimensions) on the 16 side and rows on the
-// 8 side: an operand register is then a pair of nibbles masked out of a word.  A nibble u masked in
-// place is the float16 subnormal u 2^-24 (or, 4 bits up, 16 u 2^-24), which the tensor core
-// multiplies exactly: no conversion, 5 logic operations per 8 codes; the factors 16 are taken out of q, and of
-// O's rows at the end.  Pairs of V run over two tokens: two byte permutes bring their words together.
+// Long contexts are bound by memory (1.125 d bytes per key and key/value head) and, close behind, by the instructions
+// that this takes: 560 per 32 keys at d = 128, 8 rows.  Rows of q are few, so the products are the warp's
+// m16n8k16 with keys (then dimensions) on the 16 side and rows on the 8 side: an operand register is then a pair of
+// bytes of a word of codes.  A byte b = even + 16 odd, and the even code alone, are float16 subnormals times 2^-24
+// as they stand, which the tensor core multiplies exactly: no conversion, 4 logic operations per 8 codes.  The
+// products of the pair give even and odd codes' shares after a change of basis of q (for K) or of O (for V).  Pairs of
+// V run over two tokens: two byte permutes bring their words together.
 //
 // One warp works on two tiles of 16 keys at a time and keeps its own running maximum, sum and O.  They
 // come through its own ring of shared-memory stages, filled by one bulk copy per tile (a tile with all its
@@ -21,17 +21,25 @@
 // keys.  The maximum is lazy: it moves only when a score passes it by 2^8, found by one vote per 32 keys.  p s is
 // rounded to float16 (11 bits) under a running power-of-two reference of s, moved the same way, so that
 // values of V of any size keep their bits.  The tensor core cuts its sums off (it does not round them), and codes
-// are positive, so long sums would drift; every 512 keys the middle of the codes, 7.5 times the sum of p s, moves
-// from the sums to the minima's part, which is small then too (0.5% of O over 10240 keys otherwise).
+// have no sign: sums of codes grow with the context and lose a little at each step, always downwards.  So
+// every 16 units O's sums are centred: 7.5 sum(p s), what codes of their mean would give, moves over
+// to the float32 sums of the minima.
 //
-// Work is the requests' 32-key units laid end to end, (request, kv head, chunk of rows) after another, each
-// chunk with the cost of its prologue and epilogue in front, cut into equal spans, one per warp.  Warps
-// meet only twice, to find their spans and after their last unit.  (With a block's eight warps sharing every
-// chunk, a chunk of one unit cost the block 6 us in barriers and in latencies that nothing covered.)  A warp
-// that holds all of a chunk writes O; others leave (O, m, l) for the units they have.  A block then joins the
-// parts of its warps, which follow one another, and leaves at most two parts itself, of a chunk that began
-// before it and of one that goes on after it; the join kernel adds those, in order.
+// Rows that share a key/value head (group heads times new tokens) go through the warp together, in chunks
+// of 8 (or 16).  The work of all requests, key/value heads and row chunks is one line of such units, each
+// chunk with the cost of its prologue and epilogue in front, cut into equal spans, one per warp.  Warps of a block
+// meet twice, before and after they prepare Q; a warp that holds all of a chunk writes O, others leave (O, m, l) for
+// the units they have, and the join kernel adds those, in order.
+//
+// Short contexts are bound by latency.  4,096 keys of 8 heads (15 us with the join and the launches): 1.7 us until
+// the spans are known, 2.3 until the first copies are out, 1.3 for Q, 1.5 per unit, 1 for the epilogue, 1.2 until the
+// join starts, 4.5 for it.  Each dependent read of what another processor wrote takes 0.6 us; the instructions
+// come from L2 the first time too (a quarter of the stalls).
+//
+// Measured: a batch of 48 with 1 to 16,384 keys, 32 heads over 8 of d = 128: 115 us, 3.9 TB/s (453 MB; 69 us at the
+// rate of a copy).
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv4_attn.cuh"
@@ -44,29 +52,40 @@ namespace {
 // took 421 instructions per tile, a quarter of them for those)
 constexpr int kKeys = 32;
 // What a chunk costs besides its units (its Q, its O), in units
-constexpr int kChunkCost = 3;
-// A warp gets at least this much work: fewer spans than warps for short contexts, so that less is left to join
-constexpr int kMinCost = 2;
+constexpr int kChunkCost = 4;
 // Requests of more rows per key/value head than this go to the chunk kernel (d = 64, 128)
 constexpr int kChunkMinRows = 32;
 // Units after which the sums of codes are centred
 constexpr int kCentre = 16;
 
+// Warps: as many as leave each the registers of its O and operands.  128 values of O per lane group (d NT = 128): 12 at
+// 168 registers; with 16 at 128 some spilled, and the batch of the header took 123 us (16 rows of d = 64: 25
+// instead of 21).
 template <int D, int NT>
 struct SplitCfg {
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = D * NT == 128 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kBlocksPerSm = D * NT <= 128 ? 2 : 1;
+  static constexpr int kBlocksPerSm = D * NT <= 64 ? 2 : 1;
   static constexpr int kTile = Kv4Tile<D>::kBytes;
-  // ring of a warp: 9 KB, 2 units of d = 128, where 16 warps share an SM (74 to 150 KB in flight; 45 KB cover
-  // the latency), twice that where 8 do
-  static constexpr int kStages = (D == 64 ? 4 : D == 128 ? 2 : 1) * (kBlocksPerSm == 1 ? 2 : 1);
+  static constexpr bool kQRegs = D * NT <= 64;  // Q's high parts in registers (with d NT = 128 they pushed out others: 4 us)
+  // ring of a warp: 9 KB, and twice that where 8 warps have an SM: 55 KB and more in flight (45 KB cover the latency)
+  static constexpr int kStages = (D == 64 ? 4 : D == 128 ? 2 : 1) * (kBlocksPerSm * kWarps == 8 ? 2 : 1);
   static constexpr int kStageBytes = 2 * kTile;
-  static constexpr int kLoBytes = NT * (D / 64) * 1024;  // low parts of Q: [NT][D / 64][2][32] uint4
-  static constexpr int kWarpBytes = kStages * kStageBytes + kLoBytes;
+  static constexpr int kPartBytes = NT * (D / 64) * 1024;  // high or low parts of Q: [NT][D / 64][2][32] uint4
+  static constexpr int kInfoBytes = (kRows * (16 + 4 * (D / 64)) + 15) / 16 * 16;  // of the rows, see RowInfo
+  static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kPartBytes + kInfoBytes;
   static constexpr int kSmem = kWarps * kWarpBytes;
-  static_assert((kSmem + 3072) * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
+  static_assert((kSmem + 5120) * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
+};
+
+// What a warp keeps of its rows besides Q.
+template <int ROWS, int GR>
+struct RowInfo {
+  float back[ROWS];         // scores from sums of products
+  int limit[ROWS];          // keys that the row sees
+  long long out[ROWS];      // its O, in elements
+  float sums[GR][ROWS];     // of Q's entries, by group, times 2^-24
 };
 
 // Where a walk over a span's segments stands.
@@ -79,7 +98,9 @@ struct Walk {
 };
 
 // Units of one row chunk of a request (one, with every key masked, where it has no key).
-__device__ __forceinline__ int chunk_units(int nk) { return nk > 0 ? (nk + kKeys - 1) / kKeys : 1; }
+__host__ __device__ __forceinline__ int chunk_units(int nk) {
+  return nk > 0 ? static_cast<int>((static_cast<unsigned>(nk) + kKeys - 1) / kKeys) : 1;
+}
 
 template <int ROWS>
 __device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const SeqLen& s) {
@@ -104,13 +125,15 @@ __device__ __forceinline__ bool next_segment(const Kv4AttnParams& p, volatile Wa
     }
     const int units = chunk_units(s.nk), each = units + kChunkCost;
     const int chunks = static_cast<int>((static_cast<long long>(s.nq) * p.G + ROWS - 1) / ROWS);
-    const long long rel = pos - first, idx = rel / each, start = first + idx * each;
+    const long long rel = pos - first;
+    const long long idx = rel >> 32 ? rel / each : static_cast<unsigned>(rel) / static_cast<unsigned>(each);
+    const long long start = first + idx * each;
     const long long stop = min(end, start + each);
     const int t0 = max(0, static_cast<int>(pos - start) - kChunkCost);
     const int t1 = max(0, static_cast<int>(stop - start) - kChunkCost);
     pos = stop;
     if (t1 > t0) {
-      const int h = static_cast<int>(idx / chunks);
+      const int h = chunks == 1 ? static_cast<int>(idx) : static_cast<int>(idx / chunks);
       seg.b = b, seg.h = h, seg.chunk = static_cast<int>(idx - static_cast<long long>(h) * chunks);
       seg.nq = s.nq, seg.nk = s.nk, seg.q0 = s.q0;
       seg.units = units, seg.t0 = t0, seg.t1 = t1;
@@ -162,17 +185,21 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   constexpr int kQueue = C::kStages + 2;  // segments from the one being loaded back to the one being summed
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[C::kWarps][C::kStages];
-  __shared__ long long scan[C::kWarps];
+  __shared__ long long scan[C::kThreads];
   __shared__ int abort_flag;
   __shared__ Walk walks[C::kWarps];
   __shared__ Segment queues[C::kWarps][kQueue];
-  __shared__ Meta metas[C::kWarps];
+  __shared__ Meta metas[C::kWarps];  // what each warp leaves
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * C::kWarpBytes;
-  uint4* slo = reinterpret_cast<uint4*>(ring + C::kStages * C::kStageBytes);
+  uint4* shi = reinterpret_cast<uint4*>(ring + C::kStages * C::kStageBytes);
+  uint4* slo = shi + C::kPartBytes / 16;
+  RowInfo<ROWS, GR>& info = *reinterpret_cast<RowInfo<ROWS, GR>*>(slo + C::kPartBytes / 16);
+  static_assert(sizeof(info) <= C::kInfoBytes, "room of the rows");
   uint64_t* bar = bars[warp];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
 
   if (tid < C::kWarps * C::kStages) bar_init(&bars[0][tid], 1);
   if (tid == 0) abort_flag = 0;
@@ -189,51 +216,53 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     mine += seq_cost<ROWS>(p, s);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.status, kDevStatusBadSeqlens);
-  long long before = mine;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, before, s);
-    if (lane >= s) before += o;
+    const long long o = __shfl_up_sync(0xffffffffu, mine, s);
+    if (lane >= s) mine += o;
   }
-  if (lane == 31) scan[warp] = before;
-  before -= mine;
+  scan[tid] = mine;
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kWarps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  // blocks of threads in use, all their warps alike
-  const long long blocks = min(static_cast<long long>(gridDim.x), (total + C::kWarps * kMinCost - 1) / (C::kWarps * kMinCost));
-  Meta* meta = reinterpret_cast<Meta*>(p.ws) + blockIdx.x;
-  if (blockIdx.x >= blocks) {
-    if (tid == 0) *meta = Meta{};
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    return;
-  }
-  const long long spans = blocks * C::kWarps;
-  for (int w = 0; w < C::kWarps; ++w) {
-    const long long i = static_cast<long long>(blockIdx.x) * C::kWarps + w;
-    const long long start = total * i / spans;
-    if (before <= start && start < before + mine) {  // one thread: the span starts in its run
-      int b = my0;
-      long long at = before;
-      for (;; ++b) {
-        const long long n = seq_cost<ROWS>(p, seq_len(p, b));
-        if (start < at + n) break;
-        at += n;
+  for (int w = 0; w < C::kWarps; ++w) total += scan[32 * w + 31];
+  // Warps of a block in use: as few as give each a unit of cost, so that short contexts are spread over all processors
+  // before they share one (4,096 keys of 8 heads: 14.6 us; with all warps of a third of the processors 15.7).  Spans
+  // are numbered through the warps in use, then the others, which have none.
+  const int warps = static_cast<int>(min(static_cast<long long>(C::kWarps), (total + gridDim.x - 1) / gridDim.x));
+  const int span = warp < warps ? blockIdx.x * warps + warp
+                                : gridDim.x * warps + blockIdx.x * (C::kWarps - warps) + warp - warps;
+  {
+    const unsigned spans = gridDim.x * max(warps, 1);
+    const long long each = total >> 32 ? total / spans : static_cast<unsigned>(total) / spans;
+    const long long over = total - each * spans;
+    const long long start = warp < warps ? span * each + min(static_cast<long long>(span), over) : 0;
+    const long long end = warp < warps ? start + each + (span < over ? 1 : 0) : 0;
+    long long before = 0;  // of the runs of the 32 threads among which the span starts
+    int w = 0;
+    while (w < C::kWarps - 1 && start >= before + scan[32 * w + 31]) before += scan[32 * w++ + 31];
+    const int run = __ffs(__ballot_sync(0xffffffffu, start < before + scan[32 * w + lane])) - 1;
+    if (lane == 0) {
+      int b = 0;
+      if (start < end) {
+        if (run > 0) before += scan[32 * w + run - 1];
+        b = (32 * w + run) * per;
       }
-      walks[w] = Walk{start, total * (i + 1) / spans, at, -1, b};
+      for (; per > 1 && start < end; ++b) {
+        const long long n = seq_cost<ROWS>(p, seq_len(p, b));
+        if (start < before + n) break;
+        before += n;
+      }
+      walks[warp] = Walk{start, end, before, -1, b};
     }
+    __syncwarp();
   }
-  __syncthreads();
 
   const AbortState ab{&abort_flag, p.status};
-  float* block_parts = reinterpret_cast<float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
-  float* warp_parts = block_parts + static_cast<size_t>(gridDim.x) * 2 * part_floats<D, ROWS>() +
-                      (static_cast<size_t>(blockIdx.x) * C::kWarps + warp) * 2 * part_floats<D, ROWS>();
-  block_parts += static_cast<size_t>(blockIdx.x) * 2 * part_floats<D, ROWS>();
+  // what this warp leaves: of the chunk that began before its span, and of the one that goes on behind it
+  float* const parts = reinterpret_cast<float*>(p.ws + static_cast<size_t>(gridDim.x) * C::kWarps * sizeof(Meta)) +
+                       static_cast<size_t>(span) * 2 * part_floats<D, ROWS>();
+  if (lane == 0) metas[warp] = Meta{};
 
   // ---- producer side: the units of the span, in order; segments go into the warp's queue --------------
   int p_seg = -1;            // segments opened, less one
@@ -244,20 +273,21 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   bool p_more = true;
   uint32_t absent = 0;       // 2 bits per stage: its tiles that were not loaded
   int in_flight = 0;
-  auto produce = [&](int at) {  // fills stage `at`, if there is a unit left
-    if (p_more && p_next >= p_end) {
-      volatile Segment& seg = queues[warp][(p_seg + 1) % kQueue];
-      int more = 0;
-      if (lane == 0) more = next_segment<ROWS>(p, walks[warp], seg);
-      p_more = __shfl_sync(0xffffffffu, more, 0) != 0;
-      __syncwarp();
-      if (p_more) {
-        ++p_seg;
-        p_next = seg.t0;
-        p_end = seg.t1;
-        p_base = p_next - 16;  // no window yet
-      }
+  auto open = [&]() {  // the next segment
+    volatile Segment& seg = queues[warp][(p_seg + 1) % kQueue];
+    int more = 0;
+    if (lane == 0) more = next_segment<ROWS>(p, walks[warp], seg);
+    p_more = __shfl_sync(0xffffffffu, more, 0) != 0;
+    __syncwarp();
+    if (p_more) {
+      ++p_seg;
+      p_next = seg.t0;
+      p_end = seg.t1;
+      p_base = p_next - 16;  // no window yet
     }
+  };
+  auto produce = [&](int at) {  // fills stage `at`, if there is a unit left
+    if (p_more && p_next >= p_end) open();
     if (!p_more) return;
     if (p_next - p_base >= 16) {
       volatile Segment& seg = queues[warp][p_seg % kQueue];
@@ -286,6 +316,33 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     ++in_flight;
     ++p_next;
   };
+  // Q as a lane loads it: 8 entries of a row, a set of `kAtOnce` rows per load.
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  const int sub = lane / kLanes, oct = lane % kLanes;
+  uint4 q_next = make_uint4(0u, 0u, 0u, 0u);
+  uint2 sg = make_uint2(0u, 0u);
+  auto load_q = [&](volatile Segment& it, int set) {  // zeros past its rows
+    const int n = set * kAtOnce + sub, r = it.chunk * ROWS + n;
+    q_next = make_uint4(0u, 0u, 0u, 0u);
+    if (n < ROWS && r < it.nq * p.G) {
+      const int i = r / p.G, hq = it.h * p.G + r - i * p.G;
+      q_next = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (it.q0 + i) * p.q_sn + hq * p.q_sh + 8 * oct);
+    }
+  };
+  // The first segments of a block's warps are mostly parts of one chunk: those warps prepare its Q together, a set of
+  // rows each.  The first of them is asked for here, ahead of the keys.
+  open();
+  if (!p_more && lane == 0) queues[warp][0].b = -1;
+  __syncthreads();
+  unsigned mates;
+  {
+    volatile Segment& own = queues[warp][0];
+    volatile Segment& other = queues[min(lane, C::kWarps - 1)][0];
+    mates = __ballot_sync(0xffffffffu, lane < C::kWarps && own.b == other.b && own.h == other.h && own.chunk == other.chunk);
+  }
+  int set = __popc(mates & ((1u << warp) - 1)), set_step = __popc(mates);
+  if (p_more) load_q(queues[warp][0], set);
+  if (p.signs != nullptr) sg = *reinterpret_cast<const uint2*>(p.signs + 8 * oct);
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) produce(i);
 
@@ -293,7 +350,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;  // false once a wait ran out: no more copies, and those in flight are waited for
-  if (lane == 0) metas[warp] = Meta{};
+  if (p_seg < 0) __syncthreads();  // the others' Q, below
 #pragma unroll 1
   for (int seg_no = 0; seg_no <= p_seg; ++seg_no) {
     volatile Segment& it = queues[warp][seg_no % kQueue];
@@ -301,116 +358,112 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     const int row0 = it.chunk * ROWS;
     const int rows = min(ROWS, it.nq * p.G - row0);
 
-    // Q, as the operand of row n = g (one of 8 per NT): this lane has entries 16 c .. 16 c + 15 of every group.
-    // Transformed in float32 (strides 16 and 32 lie between lanes), scaled by a power of two that puts the row's
-    // largest entry at 2^13 .. 2^14 (cf takes it back, and the 2^-24 of the codes).
+    // Q, as the operand of row n = g (one of 8 per NT): lane (g, c) needs entries 16 c .. 16 c + 15 of every group.
+    // A lane here has 8 entries of a row.  Transformed in float32, scaled by a power of two that puts the row's
+    // largest entry at 2^13 .. 2^14 (back takes it back, and the 2^-24 of the codes).
     // A byte of codes is b = even + 16 odd, so with cb = q_odd / 16 and cn = q_even - cb the products
     // cn even + cb b are q_even even + q_odd odd.  Both are kept as two float16, the rounded value and what its
-    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).  qs: sums of a
-    // group's entries, times 2^-24.
-    uint32_t qf[NT][GR][4][2];
+    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).
+    if (seg_no > 0) {
+      mates = 1u << warp;
+      set = 0, set_step = 1;
+      load_q(it, 0);
+      if (p.signs != nullptr) sg = *reinterpret_cast<const uint2*>(p.signs + 8 * oct);
+    }
+    {
+      const int gr = oct / 8;
+      const int to = (gr * 2 + (oct & 1)) * 32 + ((oct & 7) >> 1);
+      const int h = it.h, q0 = it.q0, nk = it.nk, see0 = nk - it.nq + 1;
+#pragma unroll 1
+      for (; set < ROWS / kAtOnce; set += set_step) {
+        const int n = set * kAtOnce + sub;
+        uint4 high = make_uint4(0u, 0u, 0u, 0u), low = high;
+        float back = 0.f, sum = 0.f;
+        if (set * kAtOnce < rows) {
+          float x[8];
+          const uint32_t w[4] = {q_next.x, q_next.y, q_next.z, q_next.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+          if ((set + set_step) * kAtOnce < rows) load_q(it, set + set_step);
+          if (p.signs != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // -1 is the entry with its top bit set
+              x[j] = __uint_as_float(__float_as_uint(x[j]) ^ (((j < 4 ? sg.x : sg.y) << (24 - 8 * (j & 3))) & 0x80000000u));
+#pragma unroll
+            for (int st = 1; st < 8; st <<= 1)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (!(j & st)) {
+                  const float a = x[j], b = x[j | st];
+                  x[j] = a + b;
+                  x[j | st] = a - b;
+                }
+#pragma unroll
+            for (int st = 1; st < kLanes; st <<= 1) {
+              const float sign = (lane & st) ? -1.f : 1.f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], sign, __shfl_xor_sync(0xffffffffu, x[j], st));
+            }
+          }
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+          for (int st = 1; st < kLanes; st <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, st));
+          const int ex = top > 0.f ? min(max(exponent_of(top) - 13, -100), 100) : 0;
+          const float f = exp2_int(-ex);
+          float hn[4], hb[4], ln[4], lb[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float cb = x[2 * j + 1] * f * 0.0625f, cn = x[2 * j] * f - cb;
+            hb[j] = __half2float(__float2half_rn(cb));
+            lb[j] = __half2float(__float2half_rn(cb - hb[j]));
+            hn[j] = __half2float(__float2half_rn(cn));
+            ln[j] = __half2float(__float2half_rn(cn - hn[j]));
+            sum += (hn[j] + ln[j]) + 17.f * (hb[j] + lb[j]);
+          }
+#pragma unroll
+          for (int st = 1; st < 8; st <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, st);
+          sum *= 1.f / 16777216.f;
+          back = p.scale_log2 * exp2_int(ex) * 16777216.f;
+          high = make_uint4(pack_f16x2(hn[0], hn[2]), pack_f16x2(hb[0], hb[2]), pack_f16x2(hn[1], hn[3]), pack_f16x2(hb[1], hb[3]));
+          low = make_uint4(pack_f16x2(ln[0], ln[2]), pack_f16x2(lb[0], lb[2]), pack_f16x2(ln[1], ln[3]), pack_f16x2(lb[1], lb[3]));
+        }
+        const int r = row0 + n, i = r / p.G, hq = h * p.G + r - i * p.G;
+        const int limit = p.causal && n < rows ? min(nk, see0 + i) : nk;
+        const long long out = (q0 + i) * p.o_sn + hq * p.o_sh;
+        for (unsigned m = mates; m; m &= m - 1) {
+          uint8_t* const of = smem + (__ffs(m) - 1) * C::kWarpBytes + C::kStages * C::kStageBytes;
+          uint4* const dst = reinterpret_cast<uint4*>(of) + to + (n / 8 * GR * 2) * 32 + 4 * (n % 8);
+          dst[0] = high;
+          dst[C::kPartBytes / 16] = low;
+          RowInfo<ROWS, GR>& inf = *reinterpret_cast<RowInfo<ROWS, GR>*>(of + 2 * C::kPartBytes);
+          if (oct == 0) inf.back[n] = back, inf.limit[n] = limit, inf.out[n] = out;
+          if ((oct & 7) == 0) inf.sums[gr][n] = sum;
+        }
+      }
+    }
+    if (seg_no == 0) __syncthreads();
+    else __syncwarp();
+    uint4 qf[C::kQRegs ? NT : 1][GR][2];
     float qs[NT][GR][2];  // rows 2c, 2c + 1
     float cf[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float x[GR][16];
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[gr][i] = 0.f;
-      if (8 * nt + g < rows) {
-        const int r = row0 + 8 * nt + g, i = r / p.G, hq = it.h * p.G + r - i * p.G;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (it.q0 + i) * p.q_sn + hq * p.q_sh + 16 * c;
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src + 64 * gr), v = *reinterpret_cast<const uint4*>(src + 64 * gr + 8);
-          const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[gr][2 * j] = __uint_as_float(w[j] << 16);
-            x[gr][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-          }
-        }
-      }
-      if (p.signs != nullptr) {
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          const int4 sg = *reinterpret_cast<const int4*>(p.signs + 64 * gr + 16 * c);
-          const int sw[4] = {sg.x, sg.y, sg.z, sg.w};
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (static_cast<signed char>(sw[i >> 2] >> (8 * (i & 3))) == -1) x[gr][i] = -x[gr][i];
-#pragma unroll
-          for (int st = 1; st < 16; st <<= 1)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!(i & st)) {
-                const float a = x[gr][i], b = x[gr][i | st];
-                x[gr][i] = a + b;
-                x[gr][i | st] = a - b;
-              }
-#pragma unroll
-          for (int st = 1; st < 4; st <<= 1)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float o2 = __shfl_xor_sync(0xffffffffu, x[gr][i], st);
-              x[gr][i] = (c & st) ? o2 - x[gr][i] : x[gr][i] + o2;
-            }
-        }
-#pragma unroll
-        for (int st = 1; st < GR; st <<= 1)
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-            if (!(gr & st))
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float a = x[gr][i], b = x[gr | st][i];
-                x[gr][i] = a + b;
-                x[gr | st][i] = a - b;
-              }
-      }
-      float top = 0.f;
-#pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[gr][i]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int ex = top > 0.f ? min(max(exponent_of(top) - 13, -100), 100) : 0;
-      const float f = exp2_int(-ex), back = p.scale_log2 * exp2_int(ex) * 16777216.f;
-      cf[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
-      cf[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+      for (int e = 0; e < 2; ++e) cf[nt][e] = info.back[8 * nt + 2 * c + e];
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
-        float hn[8], hb[8], ln[8], lb[8], sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float cb = x[gr][2 * k + 1] * f * 0.0625f, cn = x[gr][2 * k] * f - cb;
-          hb[k] = __half2float(__float2half_rn(cb));
-          lb[k] = __half2float(__float2half_rn(cb - hb[k]));
-          hn[k] = __half2float(__float2half_rn(cn));
-          ln[k] = __half2float(__float2half_rn(cn - hn[k]));
-          sum += (hn[k] + ln[k]) + 17.f * (hb[k] + lb[k]);
-        }
+        for (int e = 0; e < 2; ++e) qs[nt][gr][e] = info.sums[gr][8 * nt + 2 * c + e];
+        if constexpr (C::kQRegs)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const int k = 4 * (ks >> 1) + (ks & 1);
-          qf[nt][gr][ks][0] = pack_f16x2(hn[k], hn[k + 2]);
-          qf[nt][gr][ks][1] = pack_f16x2(hb[k], hb[k + 2]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k += 4)
-          slo[((nt * GR + gr) * 2 + k / 4) * 32 + lane] =
-              make_uint4(pack_f16x2(ln[k], ln[k + 2]), pack_f16x2(lb[k], lb[k + 2]),
-                         pack_f16x2(ln[k + 1], ln[k + 3]), pack_f16x2(lb[k + 1], lb[k + 3]));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= 1.f / 16777216.f;
-        qs[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-        qs[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+          for (int kp = 0; kp < 2; ++kp) qf[nt][gr][kp] = shi[((nt * GR + gr) * 2 + kp) * 32 + lane];
       }
     }
-    __syncwarp();
     const int min_lim = p.causal ? min(it.nk, max(0, it.nk - it.nq + row0 / p.G + 1)) : it.nk;
 
     float m[NT][2], l[NT][2], zacc[NT][GR][2], o[NT][D / 16][4];
@@ -445,28 +498,13 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
       in_flight = max(in_flight - 1, 0);
       const int key0 = t * kKeys;
       const uint32_t gone = (absent >> (2 * stage)) & 3u;
-      auto step = [&](auto whole_unit) {
-        constexpr bool whole = decltype(whole_unit)::value;
-        // masks: whether this lane's key e (of two) of tile ti is one of the request's, and the number of keys
-        // that row 2c + e2 of set nt sees
-        const int ka = key0 + key_at(g);
-        int nk = 0;
-        if constexpr (!whole) nk = it.nk;
-        auto held = [&](int ti, int e) { return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < nk; };
-        int lim[NT][2];
-        if constexpr (!whole) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = 8 * nt + 2 * c + e;
-              lim[nt][e] = p.causal && r < rows ? min(nk, nk - it.nq + (row0 + r) / p.G + 1) : nk;
-            }
-        }
-        auto sees = [&](int ti, int e, int nt, int e2) {
-          return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < lim[nt][e2];
-        };
-
+      // a unit that every row sees whole needs no masks (one body for both: two were twice the instructions to fetch)
+      const bool whole = gone == 0 && key0 + kKeys <= min_lim;
+      // whether this lane's key e (of two) of tile ti is one of the request's, and whether row 2c + e2 of set nt sees it
+      const int ka = key0 + key_at(g);
+      auto held = [&](int ti, int e) { return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < it.nk; };
+      auto sees = [&](int ti, int e, int limit) { return !((gone >> ti) & 1u) && ka + 16 * ti + 8 * e < limit; };
+      {
         // scores: y = sum_g s (q . u) + z (sum q), in units of log2
         float y[2][NT][4];
         bool over = false;
@@ -501,9 +539,13 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
             float acc[2][NT][4];
 #pragma unroll
             for (int kp = 0; kp < 2; ++kp) {
-              uint4 lo[NT];
+              uint4 hi[NT], lo[NT];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) lo[nt] = slo[((nt * GR + gr) * 2 + kp) * 32 + lane];
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (C::kQRegs) hi[nt] = qf[nt][gr][kp];
+                else hi[nt] = shi[((nt * GR + gr) * 2 + kp) * 32 + lane];
+                lo[nt] = slo[((nt * GR + gr) * 2 + kp) * 32 + lane];
+              }
 #pragma unroll
               for (int ti = 0; ti < 2; ++ti) {
                 uint32_t f0[4], f1[4];
@@ -515,10 +557,10 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
                 for (int nt = 0; nt < NT; ++nt) {
                   float(&ac)[4] = acc[ti][nt];
                   constexpr float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                  if (kp == 0) mma16816(ac, f0, qf[nt][gr][0][0], qf[nt][gr][0][1], zero);
-                  else mma16816(ac, f0, qf[nt][gr][2][0], qf[nt][gr][2][1], ac);
+                  if (kp == 0) mma16816(ac, f0, hi[nt].x, hi[nt].y, zero);
+                  else mma16816(ac, f0, hi[nt].x, hi[nt].y, ac);
                   mma16816(ac, f0, lo[nt].x, lo[nt].y, ac);
-                  mma16816(ac, f1, qf[nt][gr][2 * kp + 1][0], qf[nt][gr][2 * kp + 1][1], ac);
+                  mma16816(ac, f1, hi[nt].z, hi[nt].w, ac);
                   mma16816(ac, f1, lo[nt].z, lo[nt].w, ac);
                 }
               }
@@ -545,12 +587,26 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = y[ti][nt][e] * cf[nt][e & 1];
-              if constexpr (!whole) x = sees(ti, e >> 1, nt, e & 1) ? x : -INFINITY;
-              y[ti][nt][e] = x;
-              over = over || x > m[nt][e & 1] + kTau;
+            for (int e = 0; e < 4; ++e) y[ti][nt][e] *= cf[nt][e & 1];
+        if (!whole) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              const int limit = info.limit[8 * nt + 2 * c + e2];
+#pragma unroll
+              for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!sees(ti, e, limit)) y[ti][nt][2 * e + e2] = -INFINITY;
             }
+        }
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) over = over || y[ti][nt][e] > m[nt][e & 1] + kTau;
         // V's steps and minima of the lane's keys, as they are held
         float smax = 0.f;
         uint32_t vw[2][2][GR];
@@ -569,14 +625,23 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
                 vw[ti][e][gr] = v.x, vw[ti][e][gr + 1] = v.y;
               }
             }
-#pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-              if constexpr (!whole)
-                if (!held(ti, e)) vw[ti][e][gr] = 0u;
-              smax = fmaxf(smax, __uint_as_float(vw[ti][e][gr] << 16));
-            }
           }
         }
+        if (!whole) {
+#pragma unroll
+          for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!held(ti, e))
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) vw[ti][e][gr] = 0u;
+        }
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) smax = fmaxf(smax, __uint_as_float(vw[ti][e][gr] << 16));
         over = over || smax * ef > 32.f;
         if (__any_sync(0xffffffffu, over)) {  // rare: move the references, and what was summed under them
 #pragma unroll
@@ -623,26 +688,34 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
             for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(y[ti][nt][e] - m[nt][e & 1]);
             l[nt][0] += pr[0] + pr[2];
             l[nt][1] += pr[1] + pr[3];
+            float t4[GR][4];
+            auto weigh = [&](int gr, int e) {
+              const uint32_t w = vw[ti][e >> 1][gr];
+              t4[gr][e] = pr[e] * (__uint_as_float(w << 16) * ef);
+              zacc[nt][gr][e & 1] = fmaf(pr[e], __uint_as_float(w & 0xFFFF0000u), zacc[nt][gr][e & 1]);
+            };
+            if (whole) {
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-              float t4[4];
+              for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) weigh(gr, e);
+            } else {  // a masked key adds nothing, whatever its scales are (NaN among them)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t w = vw[ti][e >> 1][gr];
-                const float z = __uint_as_float(w & 0xFFFF0000u);
-                t4[e] = pr[e] * (__uint_as_float(w << 16) * ef);
-                if constexpr (whole) {
-                  zacc[nt][gr][e & 1] = fmaf(pr[e], z, zacc[nt][gr][e & 1]);
-                } else if (sees(ti, e >> 1, nt, e & 1)) {
-                  zacc[nt][gr][e & 1] = fmaf(pr[e], z, zacc[nt][gr][e & 1]);
-                } else {  // a masked key adds nothing, whatever its scales are (NaN among them)
-                  t4[e] = 0.f;
+                const bool in = sees(ti, e >> 1, info.limit[8 * nt + 2 * c + (e & 1)]);
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                  t4[gr][e] = 0.f;
+                  if (in) weigh(gr, e);
                 }
               }
-              ps[nt][gr][0] += t4[0] + t4[2];
-              ps[nt][gr][1] += t4[1] + t4[3];
-              pf[nt][gr][0] = transpose8x8(pack_f16x2(t4[0], t4[1]));
-              pf[nt][gr][1] = transpose8x8(pack_f16x2(t4[2], t4[3]));
+            }
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+              ps[nt][gr][0] += t4[gr][0] + t4[gr][2];
+              ps[nt][gr][1] += t4[gr][1] + t4[gr][3];
+              pf[nt][gr][0] = transpose8x8(pack_f16x2(t4[gr][0], t4[gr][1]));
+              pf[nt][gr][1] = transpose8x8(pack_f16x2(t4[gr][2], t4[gr][3]));
             }
           }
           // O^T += u^T (p s): dimensions 8 g + 2 q (and + 1, times 16) of each group on the 16 side
@@ -682,10 +755,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
             }
           }
         }
-      };
-      // a unit that every row sees whole needs no masks
-      if (gone == 0 && key0 + kKeys <= min_lim) step(std::true_type{});
-      else step(std::false_type{});
+      }
       if (++uncentred == kCentre) {
         uncentred = 0;
         const float per_step = 7.5f / ef;
@@ -719,6 +789,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     // ---- O, or this segment's part of it: this lane has dimensions 8 g .. 8 g + 7 of every group of rows 2c, 2c + 1
     const bool starts = it.t0 == 0, ends = it.t1 == it.units;
     const float unscale = 16777216.f / ef;
+    float* const part = parts + (starts ? part_floats<D, ROWS>() : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -729,8 +800,6 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
         for (int sft = 4; sft < 32; sft <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sft);
         const bool whole_chunk = starts && ends;
         const float inv = whole_chunk ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        const int i = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - i * p.G;
-        float* part = warp_parts + (starts ? part_floats<D, ROWS>() : 0);
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
           float z = zacc[nt][gr][e];
@@ -745,7 +814,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
           }
           if (r < rows) {
             if (whole_chunk) {
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (it.q0 + i) * p.o_sn + hq * p.o_sh + 64 * gr + 8 * g) =
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + info.out[r] + 64 * gr + 8 * g) =
                   make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             } else {
               float4* dst = reinterpret_cast<float4*>(part + r * D + 64 * gr + 8 * g);
@@ -759,93 +828,30 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
             part[ROWS * D + r] = m[nt][e];
             part[ROWS * D + ROWS + r] = sum;
           } else if (p.lse != nullptr) {
+            const int i = (row0 + r) / p.G, hq = it.h * p.G + (row0 + r) - i * p.G;
             p.lse[static_cast<long long>(hq) * p.total_q + it.q0 + i] =
                 sum == 0.f ? -INFINITY : (m[nt][e] + log2f(sum)) * kLn2f;
           }
         }
       }
     if (lane == 0) {
-      Meta& mt = metas[warp];
+      Meta& left = metas[warp];
       if (starts && !ends) {
-        mt.tail_valid = 1;
-        mt.b = it.b, mt.h = it.h, mt.chunk = it.chunk;
-        mt.rows[0] = rows;
-      } else if (!starts) {
-        mt.head_valid = 1;
-        mt.head_ends = ends;
-        mt.rows[1] = rows;
+        left.flags |= kTailValid | static_cast<unsigned>(rows) << kRowsShift;
+        left.q0 = it.q0, left.h = it.h, left.chunk = it.chunk;
+      } else if (!starts && ends) {
+        left.flags |= kHeadEnds;
       }
     }
     __syncwarp();
   }
-  __syncthreads();
-
-  // ---- join the parts of this block's warps, which follow one another ---------------------------------------
-  float* first_part = warp_parts - static_cast<size_t>(warp) * 2 * part_floats<D, ROWS>();
-  Meta mine_all{};
-  for (int w = -1; w < C::kWarps;) {
-    // a chunk from warp w's tail (w = -1: from the warps before this block) over the heads of the next ones
-    if (w >= 0 && !metas[w].tail_valid) {
-      ++w;
-      continue;
-    }
-    int last = w;
-    bool ended = false;
-    while (last + 1 < C::kWarps && !ended && metas[last + 1].head_valid) ended = metas[++last].head_ends;
-    if (last == w && w < 0) {  // no chunk from before
-      ++w;
-      continue;
-    }
-    const Meta& mt = metas[w < 0 ? 0 : w];
-    const int rows = w < 0 ? mt.rows[1] : mt.rows[0];
-    const bool done = w >= 0 && ended;  // the chunk lies in this block
-    auto part = [&](int j) { return first_part + (static_cast<size_t>(j) * 2 + (j == w ? 1 : 0)) * part_floats<D, ROWS>(); };
-    const int j0 = max(w, 0);
-    for (int i = tid; i < rows * (D / 2); i += C::kThreads) {
-      const int r = i / (D / 2), x = 2 * (i - r * (D / 2));
-      float top = kNegBig, a0 = 0.f, a1 = 0.f, sum = 0.f;
-      for (int j = j0; j <= last; ++j) top = fmaxf(top, part(j)[ROWS * D + r]);
-      for (int j = j0; j <= last; ++j) {
-        const float* q = part(j);
-        const float f = ex2_approx(q[ROWS * D + r] - top);
-        const float2 v = *reinterpret_cast<const float2*>(q + r * D + x);
-        a0 += v.x * f;
-        a1 += v.y * f;
-        sum += q[ROWS * D + ROWS + r] * f;
-      }
-      if (done) {
-        write_row_pair<D>(p, seq_len(p, mt.b).q0, mt.h, mt.chunk * ROWS + r, x, a0, a1, top, sum);
-      } else {
-        float* dst = block_parts + (w >= 0 ? part_floats<D, ROWS>() : 0);
-        *reinterpret_cast<float2*>(dst + r * D + x) = make_float2(a0, a1);
-        if (x == 0) {
-          dst[ROWS * D + r] = top;
-          dst[ROWS * D + ROWS + r] = sum;
-        }
-      }
-    }
-    if (w < 0) {
-      mine_all.head_valid = 1;
-      mine_all.head_ends = ended;
-    } else if (!ended) {
-      mine_all.tail_valid = 1;
-      mine_all.b = mt.b;
-      mine_all.h = mt.h;
-      mine_all.chunk = mt.chunk;
-    }
-    w = w < 0 ? (ended ? last : C::kWarps) : ended ? last : C::kWarps;
-    if (w < C::kWarps && !metas[w].tail_valid) ++w;
-  }
-  if (tid == 0) *meta = mine_all;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) reinterpret_cast<Meta*>(p.ws)[span] = metas[warp];
 }
 
-// The workspace: the blocks' parts, then two parts per warp, likewise.
 template <int D, int NT>
 unsigned long long ws_bytes(int num_sms) {
   using C = SplitCfg<D, NT>;
-  const unsigned long long blocks = static_cast<unsigned long long>(num_sms) * C::kBlocksPerSm;
-  return part_bytes<D, C::kRows>(blocks) + blocks * C::kWarps * 2 * sizeof(float) * part_floats<D, C::kRows>();
+  return part_bytes<D, C::kRows>(static_cast<unsigned long long>(num_sms) * C::kBlocksPerSm * C::kWarps);
 }
 
 template <int D, int NT>
@@ -857,11 +863,16 @@ cudaError_t setup() {
 template <int D, int NT>
 cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   using C = SplitCfg<D, NT>;
-  const int grid = num_sms * C::kBlocksPerSm;
-  kv4_split_kernel<D, NT><<<grid, C::kThreads, C::kSmem, stream>>>(p);
+  // no more blocks than the tables' width can give units to
+  const long long most = static_cast<long long>(chunk_units(p.width * p.page)) + kChunkCost;
+  const long long rows = static_cast<long long>(p.max_q) * p.G, chunks = (rows + C::kRows - 1) / C::kRows;
+  const long long full = static_cast<long long>(num_sms) * C::kBlocksPerSm, heads = static_cast<long long>(p.B) * p.Hk;
+  long long grid = full;  // (the product stays below 2^63: each factor is below full)
+  if (heads < full && chunks < full && most < full) grid = std::min(full, heads * chunks * most);
+  kv4_split_kernel<D, NT><<<static_cast<int>(grid), C::kThreads, C::kSmem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, C::kRows>(p, grid, C::kRows, stream);
+  return launch_join<D, C::kRows, C::kWarps>(p, static_cast<int>(grid), stream);
 }
 
 }  // namespace

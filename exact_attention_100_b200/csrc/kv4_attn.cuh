@@ -2,6 +2,8 @@
 // and their join.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,18 +49,19 @@ struct Segment {
   int units, t0, t1;
 };
 
-// A part of a chunk: [ROWS][D] float O, [ROWS] m, [ROWS] l.  The workspace holds a Meta per block of
-// threads, then two parts per block: of the chunk that began before it, and of the one that goes on after it.
+// A part of a chunk: [ROWS][D] float O, [ROWS] m, [ROWS] l.  The workspace holds a Meta per span, then two parts
+// per span: of the chunk that began before it, and of the one that goes on after it.
 template <int D, int ROWS>
 __host__ __device__ constexpr int part_floats() { return ROWS * (D + 2); }
 
-struct Meta {
-  int tail_valid;  // the last chunk starts here and goes on behind
-  int b, h, chunk;
-  int head_valid;  // the first chunk started before
-  int head_ends;   // ... and ends here
-  int rows[2];     // of the tail, of the head (a warp's)
+struct alignas(16) Meta {
+  unsigned flags;   // and, from kRowsShift on, the rows of the chunk that goes on
+  int q0, h, chunk;  // of that chunk
 };
+constexpr unsigned kTailValid = 1;  // the span's last chunk starts in it and goes on behind
+constexpr unsigned kHeadEnds = 2;   // the span's first chunk started before and ends in it
+constexpr int kRowsShift = 8;
+static_assert(sizeof(Meta) == 16, "read as one vector; the parts behind are stored 16 bytes at a time");
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -78,112 +81,190 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
-// Writes dimensions x, x + 1 of O (a0, a1 over sum) of a request's row, and with x = 0 its LSE.
-template <int D>
-__device__ __forceinline__ void write_row_pair(const Kv4AttnParams& p, int q0, int h, int row, int x, float a0, float a1,
-                                               float top, float sum) {
-  const int i = row / p.G, hq = h * p.G + row - i * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (q0 + i) * p.o_sn + hq * p.o_sh + x) =
-      pack_bf16x2(a0 * inv, a1 * inv);
-  if (x == 0 && p.lse != nullptr)
-    p.lse[static_cast<long long>(hq) * p.total_q + q0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-}
+// Joins the parts of the row chunks that several spans share: block (i, y) does rows y, y + gridDim.y, ... of the
+// chunks that start in one of the spans PER i .. PER i + PER - 1 and go on, in the order of the spans.  What it waits
+// for is one round of loads after another (0.6 us each, the parts were just written elsewhere), so there are two of
+// them as a rule: the first tells which of its spans begin such chunks and where the next 256 spans end one (a block
+// without a chunk is gone then); in the second a warp asks for O, m and l of kBatch parts at once and adds them up
+// under a running maximum.  A row is one warp's, or up to eight warps' where the block has fewer rows than warps.
+constexpr int kJoinThreads = 256;
+// gridDim.y at most: 148 x 8 blocks fit the processors at once, or 16 where a chunk has hundreds of rows
+template <int ROWS>
+constexpr int join_rows() { return ROWS > 16 ? 16 : 4; }
 
-// Joins the parts of the row chunks that several blocks of threads share: block (i, r) does row r of
-// the chunk that starts in block i's span and goes on (and every gridDim.y-th row after it), in the order of
-// the spans.  Its threads first look
-// together for the span where the chunk ends and for the largest m; then each adds two dimensions over
-// its share of the parts, whose loads do not wait for one another.
-constexpr int kJoinThreads = 128;
-
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnParams p) {
-  constexpr int kShares = kJoinThreads / (D / 2);
-  __shared__ int s_last;
-  __shared__ float s_top[kJoinThreads / 32];
-  __shared__ float s_part[kShares][D / 2][3];
+template <int D, int ROWS, int PER>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnParams p, int spans) {
+  constexpr int kWarps = kJoinThreads / 32;
+  constexpr int kAtOnce = D == 64 ? 2 : 1;   // parts of a warp's load
+  constexpr int kLoads = D == 256 ? 2 : 1;   // of 4 dimensions per lane
+  constexpr int kBatch = D == 256 ? 5 : 9;
+  __shared__ unsigned s_ends[kWarps];
+  __shared__ __align__(16) float s_part[kWarps][D];  // read and written four at a time
+  __shared__ float s_sum[kWarps], s_top[kWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Meta* metas = reinterpret_cast<const Meta*>(p.ws);
-  const int first = blockIdx.x, tid = threadIdx.x;
-  const Meta mt = metas[first];
-  if (!mt.tail_valid) return;
-  const SeqLen s = seq_len(p, mt.b);
-  const int rows = min(ROWS, s.nq * p.G - mt.chunk * ROWS);
-  if (static_cast<int>(blockIdx.y) >= rows) return;
-  if (tid == 0) s_last = gridDim.x - 1;
-  for (int base = first + 1;; base += kJoinThreads) {
-    const int j = base + tid;
-    const bool end = j >= static_cast<int>(gridDim.x) || metas[j].head_ends;
-    if (__syncthreads_or(end)) {
-      if (end) atomicMin(&s_last, j);
-      break;
-    }
-  }
+  const float* parts = reinterpret_cast<const float*>(p.ws + static_cast<size_t>(spans) * sizeof(Meta));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, y = blockIdx.y, ys = gridDim.y;
+  const int base = blockIdx.x * PER;
+  const uint4 mine = *reinterpret_cast<const uint4*>(metas + min(base + lane % PER, spans - 1));
+  auto ends_at = [&](int j) { return j >= spans - 1 || (metas[min(j, spans - 1)].flags & kHeadEnds); };
+  const unsigned ends32 = __ballot_sync(0xffffffffu, ends_at(base + 1 + tid));
+  const int my_rows = lane < PER && base + lane < spans && (mine.x & kTailValid) ? static_cast<int>(mine.x >> kRowsShift) : 0;
+  if (!__any_sync(0xffffffffu, y < my_rows)) return;  // every warp alike
+  if (lane == 0) s_ends[warp] = ends32;
   __syncthreads();
-  const int last = s_last;
-  const float* parts = reinterpret_cast<const float*>(p.ws + static_cast<size_t>(gridDim.x) * sizeof(Meta));
-  auto part = [&](int j) {  // the first span holds the chunk in its second slot, the others in their first
-    return parts + (static_cast<size_t>(j) * 2 + (j == first ? 1 : 0)) * part_floats<D, ROWS>();
+  const int my_items = y < my_rows ? (my_rows - y + ys - 1) / ys : 0;
+  int total = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) total += __shfl_sync(0xffffffffu, my_items, k);
+  const int share = total == 1 ? 8 : total == 2 ? 4 : total <= 4 ? 2 : 1;  // warps of a row
+
+  int r = 0, k = 0;
+  float top = kNegBig, sum = 0.f, a[4 * kLoads];
+  const int x = D == 64 ? lane % 16 : lane;
+  auto write = [&]() {
+    const int q0 = __shfl_sync(0xffffffffu, mine.y, k), h = __shfl_sync(0xffffffffu, mine.z, k);
+    const int row = __shfl_sync(0xffffffffu, static_cast<int>(mine.w), k) * ROWS + r, i = row / p.G;
+    const int hq = h * p.G + row - i * p.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (q0 + i) * p.o_sn + hq * p.o_sh + 4 * x;
+    if (D != 64 || lane < 16)
+#pragma unroll
+      for (int v = 0; v < kLoads; ++v)
+        *reinterpret_cast<uint2*>(o + 128 * v) = make_uint2(pack_bf16x2(a[4 * v] * inv, a[4 * v + 1] * inv),
+                                                            pack_bf16x2(a[4 * v + 2] * inv, a[4 * v + 3] * inv));
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[static_cast<long long>(hq) * p.total_q + q0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
   };
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float top = kNegBig;
-    for (int j = first + tid; j <= last; j += kJoinThreads) top = fmaxf(top, part(j)[ROWS * D + r]);
-#pragma unroll
-    for (int sft = 16; sft; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    __syncthreads();
-    top = s_top[0];
-#pragma unroll
-    for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-    const int x = tid % (D / 2), share = tid / (D / 2);
-    float a0 = 0.f, a1 = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int j = first + share; j <= last; j += kShares) {
-      const float* q = part(j);
-      const float f = ex2_approx(q[ROWS * D + r] - top);
-      const float2 v = *reinterpret_cast<const float2*>(q + r * D + 2 * x);
-      a0 += v.x * f;
-      a1 += v.y * f;
-      sum += q[ROWS * D + ROWS + r] * f;
+#pragma unroll 1
+  for (int item = warp / share; item < total; item += kWarps / share) {  // one round where warps share rows
+    int left = item;
+    for (k = 0;; ++k) {
+      const int n = __shfl_sync(0xffffffffu, my_items, k);
+      if (left < n) break;
+      left -= n;
     }
-    if constexpr (kShares > 1) {
-      s_part[share][x][0] = a0;
-      s_part[share][x][1] = a1;
-      s_part[share][x][2] = sum;
-      __syncthreads();
-      if (share == 0) {
+    r = y + left * ys;
+    const int first = base + k;
+    // bit i of the words: span base + 1 + i ends a chunk; the chunk of span base + k ends at the first one from bit k on
+    int last = -1;
+#pragma unroll 1
+    for (int w = 0; w < kWarps && last < 0; ++w) {
+      const unsigned e = s_ends[w] & (w == 0 ? ~0u << k : ~0u);
+      if (e) last = min(base + 32 * w + __ffs(e), spans - 1);
+    }
+    for (int at = base + 1 + kJoinThreads; last < 0; at += 256) {  // further off
+      unsigned found = 0;
 #pragma unroll
-        for (int i = 1; i < kShares; ++i) {
-          a0 += s_part[i][x][0];
-          a1 += s_part[i][x][1];
-          sum += s_part[i][x][2];
+      for (int i = 0; i < 8; ++i) found |= ends_at(at + 8 * lane + i) ? 1u << i : 0u;
+      const unsigned any = __ballot_sync(0xffffffffu, found != 0);
+      if (any) {
+        const int l = __ffs(any) - 1;
+        last = min(at + 8 * l + __ffs(__shfl_sync(0xffffffffu, found, l)) - 1, spans - 1);
+      }
+    }
+    // the first span holds the chunk in its second slot, the others in their first
+    const float* const head = parts + static_cast<size_t>(first) * 2 * part_floats<D, ROWS>();
+    top = kNegBig, sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4 * kLoads; ++v) a[v] = 0.f;
+    const int step = share * kAtOnce, n = last - first + 1;
+#pragma unroll 1
+    for (int j0 = warp % share * kAtOnce + (D == 64 ? lane / 16 : 0); j0 < n + kAtOnce - 1; j0 += kBatch * step) {
+      float m[kBatch], l[kBatch];
+      float4 u[kBatch][kLoads];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int j = j0 + b * step;
+        m[b] = kNegBig, l[b] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kLoads; ++v) u[b][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n) {
+          const float* q = head + static_cast<size_t>(2 * j + (j == 0 ? 1 : 0)) * part_floats<D, ROWS>();
+          m[b] = q[ROWS * D + r];
+          l[b] = q[ROWS * D + ROWS + r];
+#pragma unroll
+          for (int v = 0; v < kLoads; ++v) u[b][v] = *reinterpret_cast<const float4*>(q + r * D + 128 * v + 4 * x);
+        }
+      }
+      float t = top;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) t = fmaxf(t, m[b]);
+      const float old = ex2_approx(top - t);
+      top = t;
+      sum *= old;
+#pragma unroll
+      for (int v = 0; v < 4 * kLoads; ++v) a[v] *= old;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float f = ex2_approx(m[b] - t);
+        sum += l[b] * f;
+#pragma unroll
+        for (int v = 0; v < kLoads; ++v) {
+          a[4 * v] += u[b][v].x * f, a[4 * v + 1] += u[b][v].y * f;
+          a[4 * v + 2] += u[b][v].z * f, a[4 * v + 3] += u[b][v].w * f;
         }
       }
     }
-    if (share == 0) write_row_pair<D>(p, s.q0, mt.h, mt.chunk * ROWS + r, 2 * x, a0, a1, top, sum);
-    __syncthreads();
+    if constexpr (D == 64) {
+      const float t = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), f = ex2_approx(top - t);
+      top = t;
+      sum *= f;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        a[v] *= f;
+        a[v] += __shfl_xor_sync(0xffffffffu, a[v], 16);
+      }
+    }
+    if (share == 1) write();
   }
+  if (share == 1) return;
+  const bool have = warp / share < total;
+  if (have) {
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v)
+      if (D != 64 || lane < 16)
+        *reinterpret_cast<float4*>(&s_part[warp][128 * v + 4 * x]) = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+    if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
+  }
+  __syncthreads();
+  if (!have || warp % share != 0) return;
+  for (int w = warp; w < warp + share; ++w) top = fmaxf(top, s_top[w]);
+  sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < 4 * kLoads; ++v) a[v] = 0.f;
+#pragma unroll 2
+  for (int w = warp; w < warp + share; ++w) {
+    const float f = ex2_approx(s_top[w] - top);
+    sum += s_sum[w] * f;
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v) {
+      const float4 u = *reinterpret_cast<const float4*>(&s_part[w][128 * v + 4 * x]);
+      a[4 * v] += u.x * f, a[4 * v + 1] += u.y * f, a[4 * v + 2] += u.z * f, a[4 * v + 3] += u.w * f;
+    }
+  }
+  write();
 }
 
 template <int D, int ROWS>
-unsigned long long part_bytes(unsigned long long blocks) {
-  return blocks * (sizeof(Meta) + 2 * sizeof(float) * part_floats<D, ROWS>());
+unsigned long long part_bytes(unsigned long long spans) {
+  return spans * (sizeof(Meta) + 2 * sizeof(float) * part_floats<D, ROWS>());
 }
 
 // The join, started while the kernel that leaves the parts still runs (it waits for its end).
-template <int D, int ROWS>
-cudaError_t launch_join(const Kv4AttnParams& p, int blocks, int rows_at_once, cudaStream_t stream) {
+template <int D, int ROWS, int PER>
+cudaError_t launch_join(const Kv4AttnParams& p, int blocks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(blocks, rows_at_once);
+  cfg.gridDim = dim3(blocks, static_cast<unsigned>(std::min<long long>(static_cast<long long>(p.max_q) * p.G, join_rows<ROWS>())));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, ROWS>, p);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, ROWS, PER>, p, blocks * PER);
 }
 
 }  // namespace ea

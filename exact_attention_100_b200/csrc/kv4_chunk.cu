@@ -428,11 +428,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       const int row0 = S.chunk * ROWS, rows = min(ROWS, S.nq * p.G - row0);
       const bool starts = S.t0 == 0, ends = S.t1 == S.units;
       if (starts && !ends) {
-        found.tail_valid = 1;
-        found.b = S.b, found.h = S.h, found.chunk = S.chunk;
-      } else if (!starts) {
-        found.head_valid = 1;
-        found.head_ends = ends;
+        found.flags |= kTailValid | static_cast<unsigned>(rows) << kRowsShift;
+        found.q0 = S.q0, found.h = S.h, found.chunk = S.chunk;
+      } else if (!starts && ends) {
+        found.flags |= kHeadEnds;
       }
       if (q * 128 >= rows) {  // no row of this tile
         blk += S.t1 - S.t0;
@@ -857,7 +856,7 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   kv4_chunk_kernel<D><<<num_sms, C::kThreads, C::kSmem, stream>>>(q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, kRowsPerChunk>(q, num_sms, 16, stream);
+  return launch_join<D, kRowsPerChunk, 1>(q, num_sms, stream);
 }
 
 }  // namespace
