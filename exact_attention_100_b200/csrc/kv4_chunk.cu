@@ -8,11 +8,22 @@
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: one thread per row; writes O
 //   warps 8-15       codes of K to float16 tiles (128-byte swizzle), then those of V, 4 threads per key
-//   warp 16          one thread issues every tcgen05.mma
+//   warp 16          one lane issues every tcgen05.mma
 //   warp 17          copies Q, and tiles of the cache (one bulk copy each) into a ring of three and a half blocks
+//   warp 18          looks at the scales of a block as soon as it is there: its largest values, what is missing
 // K and V tiles take turns in three slots: V of a block is brought in while its S runs, K of the next one while
-// its P.V does.  Five warps of different roles share a scheduler, so each role's loop is kept short: with the loops
-// unrolled (160 KB of code) a third of the cycles went by without an instruction.
+// its P.V does.  Five or six warps of different roles share a scheduler and its instruction buffer, so each role's loop
+// is kept short: with the loops unrolled (160 KB of code) a third of the cycles went by without an instruction, and
+// with the softmax loop alone unrolled from 64 keys to a whole block the kernel takes a fifth longer.
+// The whole of warp 16 goes through its loop and a lane is elected only around the products: their descriptors are then
+// the same for all lanes as the compiler sees it (80 cycles per product to issue instead of 104; it takes 64).
+//
+// Measured: 1,000 to 2,048 new tokens of two requests over 8,192 to 10,240 keys, 32 heads over 8 of d = 128: 561 us,
+// 776 TFLOP/s (1,012 is what the kernel for bf16 K and V makes of this shape).  A block of 128 keys takes 4,900 cycles;
+// its exponentials and its products each need 2,048.  What is left is the chain of one tile: its softmax, 2,600
+// (two warps of a scheduler share the special-function unit), then its P.V and its next S, which use the same
+// columns of tensor memory.  Tried without gain: S of 64 keys twice buffered, one issuing warp per tile, waiting for K
+// between P.V and S.
 //
 // Every operand is float16 (11 bits): Q, each row scaled by a power of two; K and V, u s + z in one fused
 // multiply-add, scaled by a power of two that puts the block's largest value (K) or the largest so far (V, O moves
@@ -44,7 +55,7 @@ constexpr int kMinCost = 2;
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int kThreads = 576;
+  static constexpr int kThreads = 608;
   static constexpr int kBoxes = D / 64;                 // 64-dimension halves, rows of 128 bytes
   static constexpr int kBoxBytes = 128 * 128;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;  // 128 rows x D float16
@@ -60,13 +71,16 @@ struct ChunkCfg {
   static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
 };
 
-// What the softmax needs to know of a block of keys
-struct BlockInfo {
-  float k_back;  // K was scaled by its inverse
-  int v_exp;     // V was scaled by 2^-v_exp
-  uint32_t gone;  // bit i: tile i of the block is not there (a table entry out of range)
-  uint32_t odd[4];  // one bit per key: its V is not finite (and is held as zero in shared memory)
+// What is known of a block of keys from its scales
+struct alignas(16) BlockInfo {
+  float k_back;      // K is held scaled by its inverse
+  int v_exp;         // V is held scaled by 2^-v_exp
+  uint32_t gone;     // bit i: tile i of the block is not there (a table entry out of range)
+  uint32_t special;  // not zero: some tile is not there, or some V is not finite
+  uint32_t odd[4];   // one bit per key: its V is not finite (and is held as zero in shared memory)
 };
+// Of them: the block that is read for, three in the ring of tiles, and the one whose softmax runs
+constexpr int kInfos = 8;
 
 struct ChunkWalk {
   long long pos, end;  // of the span
@@ -184,25 +198,23 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]
       : "r"(taddr) : "memory");
 }
 
-// p = 2^(s c + nm) of 32 keys: packed float16 in pk, their sums added to acc; returns the largest of them as float16
-// (positive ones compare as their bits).  All exponentials on the special-function unit: 2,048 of its cycles per block
-// and scheduler; a quarter of them as a cubic on the FMA pipe, as in the bf16 forward, took 14 more instructions a pair
-// and was slower.
-__device__ __forceinline__ uint32_t exps(const uint32_t (&r)[32], uint32_t (&pk)[16], float (&acc)[4], float c, float nm) {
-  uint32_t top[2] = {0u, 0u};
+// p = 2^(s c + nm) of 32 keys: packed float16 in pk; returns their sum.  All exponentials on the
+// special-function unit: 2,048 of its cycles per block and scheduler; a quarter of them as a cubic on the FMA pipe, as
+// in the bf16 forward, took 14 more instructions a pair and was slower.
+__device__ __forceinline__ float exps(const uint32_t (&r)[32], uint32_t (&pk)[16], float c, float nm) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float x0, x1;
     fma2_bcast(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), c, nm);
     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-    add2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], p0, p1);
+    add2(s[2 * (i & 1)], s[2 * (i & 1) + 1], p0, p1);
     pk[i] = pack_f16x2(p0, p1);
-    asm("max.f16x2 %0, %0, %1;" : "+r"(top[i & 1]) : "r"(pk[i]));
   }
-  asm("max.f16x2 %0, %0, %1;" : "+r"(top[0]) : "r"(top[1]));
-  return max(top[0] & 0xFFFFu, top[0] >> 16);
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
-constexpr uint32_t kTauF16 = 0x5C00u;  // 2^kTau
+// The reference moves when the p of 32 keys come to more than this (no one of them is more, then, if they do not)
+constexpr float kSumMost = 256.f;
 
 // Q of a chunk of rows as the products take it: two tiles of 128 rows x D float16 as they lie in shared memory, then
 // [256] factors of the rows' scores, written ahead by kv4_chunk_q_kernel.  Request b's chunks start at q0 G / 256 + b,
@@ -299,13 +311,10 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
   }
 }
 
-// A barrier of warps 8-15: whether all of them say yes.
-__device__ __forceinline__ bool codes_all(bool v) {
+// One lane of a warp, always the same, in a way that lets the others' registers count as uniform.
+__device__ __forceinline__ bool elect_one() {
   uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
 
@@ -319,11 +328,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   __shared__ uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots];
   __shared__ uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drained;
   __shared__ uint32_t raw_gone[C::kRawSlots];
-  __shared__ BlockInfo info[2];
-  __shared__ float wmax[2][8];
-  __shared__ uint32_t wodd[2][4];
+  __shared__ BlockInfo info[kInfos];
+  __shared__ uint64_t info_full[kInfos];
   __shared__ long long scan[C::kThreads / 32];
-  __shared__ ChunkWalk walks[18];
+  __shared__ ChunkWalk walks[19];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -344,6 +352,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       bar_init(&p_full[i], 4);
       bar_init(&o_done[i], 1);
     }
+    for (int i = 0; i < kInfos; ++i) bar_init(&info_full[i], 1);
     bar_init(&drained, 1);
     abort_flag = 0;
     fence_barrier_init();
@@ -391,7 +400,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       if (span0 < before + n) break;
       before += n;
     }
-    for (int w = 0; w < 18; ++w) {
+    for (int w = 0; w < 19; ++w) {
       walks[w].pos = span0;
       walks[w].end = span1;
       walks[w].first = before;
@@ -449,23 +458,49 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       float m = kNegBig, l = 0.f;
       int v_exp = 0;
       for (int t = S.t0; t < S.t1; ++t, ++blk, ++sit) {
-        // V of the block as well: its exponent goes into this block's P
-        const uint32_t v_item = 2 * blk + 1;
-        ok = warp_all(wait_bar(&s_full[q], sit & 1u, ab) &&
-                      wait_bar(&kv_full[v_item % C::kSlots], (v_item / C::kSlots) & 1u, ab));
+        // the block's scales too: V's exponent goes into this block's P
+        ok = warp_all(wait_bar(&info_full[blk % kInfos], (blk / kInfos) & 1u, ab) && wait_bar(&s_full[q], sit & 1u, ab));
         if (!ok) break;
         tc_fence_after();
-        const volatile BlockInfo& bi = info[blk & 1u];
-        const float c = c_row * bi.k_back;
+        const BlockInfo& bi = info[blk % kInfos];
+        const uint4 known = *reinterpret_cast<const uint4*>(&bi);
+        const float c = c_row * __uint_as_float(known.x);
+        const int ve = static_cast<int>(known.y);
         const int lim = lim_row - t * kBlockKeys;
-        const uint32_t gone = bi.gone, odds = bi.odd[0] | bi.odd[1] | bi.odd[2] | bi.odd[3];
-        const bool need_mask = (t + 1) * kBlockKeys > lim_first || (gone | odds) != 0;
+        const bool need_mask = (t + 1) * kBlockKeys > lim_first || known.w != 0;
         float alpha = 1.f;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        // 32 keys at a time, p under the reference at hand; only where one comes out above 2^kTau the reference moves,
+        float l_blk = 0.f;  // of p under the reference at hand
+        // 32 keys at a time, p under the reference at hand; only where they come to too much the reference moves,
         // and with it what was done under it.  P of 32 keys overwrites 16 columns of S that have been read.
+        // A block that every row of the tile sees whole goes through a loop of 64 keys, without masks and with its loads
+        // together; keys from the first ones that come to too much on, and blocks with masks, take the other one.
+        int k0 = 0;
+        if (!need_mask) {
+          bool over = false;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
+          for (int k2 = 0; k2 < 4 && !over; k2 += 2) {
+            uint32_t a[32], b[32], pk[16];
+            tmem_ld_32cols(tS + 32 * k2, a);
+            tmem_ld_32cols(tS + 32 * k2 + 32, b);
+            tmem_ld_wait(a);
+            tmem_ld_wait(b);
+            const float sa = exps(a, pk, c, -m);
+            over = __any_sync(0xffffffffu, sa > kSumMost);
+            if (over) break;
+            l_blk += sa;
+            tmem_st_16cols(tS + 16 * k2, pk);
+            k0 = k2 + 1;
+            const float sb = exps(b, pk, c, -m);
+            over = __any_sync(0xffffffffu, sb > kSumMost);
+            if (over) break;
+            l_blk += sb;
+            tmem_st_16cols(tS + 16 * k2 + 16, pk);
+            k0 = k2 + 2;
+          }
+        }
+        const bool moved = k0 < 4;
+#pragma unroll 1
+        for (int k = k0; k < 4; ++k) {
           uint32_t r[32], pk[16];
           tmem_ld_32cols(tS + 32 * k, r);
           tmem_ld_wait(r);
@@ -474,12 +509,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               if ((odd >> i) & 1u) r[i] = 0x7FC00000u;  // a V that is not finite makes the rows that see it NaN
-              if (32 * k + i >= lim || ((gone >> (2 * k + (i >> 4))) & 1u)) r[i] = __float_as_uint(-INFINITY);
+              if (32 * k + i >= lim || ((known.z >> (2 * k + (i >> 4))) & 1u)) r[i] = __float_as_uint(-INFINITY);
             }
           }
-          const float before[4] = {acc[0], acc[1], acc[2], acc[3]};
-          const uint32_t top = exps(r, pk, acc, c, -m);
-          if (__any_sync(0xffffffffu, top > kTauF16)) {
+          float sum = exps(r, pk, c, -m);
+          if (__any_sync(0xffffffffu, sum > kSumMost)) {
             float mx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
@@ -495,8 +529,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
             }
             alpha *= a;
             l *= a;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = before[i] * a;
+            l_blk *= a;
             const uint32_t a2 = pack_f16x2(a, a);
             tmem_st_wait();
 #pragma unroll 1
@@ -507,16 +540,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
               for (int i = 0; i < 16; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(old[i]) : "r"(a2));
               tmem_st_16cols(tS + 16 * j, old);
             }
-            exps(r, pk, acc, c, -m);
+            sum = exps(r, pk, c, -m);
           }
+          l_blk += sum;
           tmem_st_16cols(tS + 16 * k, pk);
         }
-        l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        l += l_blk;
         tmem_st_wait();
-        const int ve = bi.v_exp;
         if (t > S.t0 && ve != v_exp) alpha *= exp2_int(max(v_exp - ve, -126));
+        const bool scaled = t > S.t0 && (moved || ve != v_exp);
         v_exp = ve;
-        if (__any_sync(0xffffffffu, alpha != 1.f) && t > S.t0) {
+        if (scaled && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O *= alpha: the P.V of the block before has completed (it was issued before this block's S)
           tc_fence_after();
 #pragma unroll 1
@@ -590,52 +624,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
     bool ok = true;
     Segment S;
     while (ok && take_segment(p, walks[warp], lane, S)) {
-      int exp_v = -100;  // of V: the largest so far
       for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += 4) {
-#pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i)
-          ok = warp_all(wait_bar(&raw_full[(pair + i) % C::kRawSlots], ((pair + i) / C::kRawSlots) & 1u, ab));
-        // the block's largest values: one key per thread, K's in the first four warps and V's in the others; a key that
-        // is not there, or not finite, counts as zero
-        float top = 0.f;
-        bool odd = false;
-        if (ok) {
-          const int key = ct & 127;
-          const uint32_t rs = (pair + (key >> 5)) % C::kRawSlots;
-          const int tj = (key >> 4) & 1;
-          const uint8_t* sz = smem + C::kRawOff + rs * C::kRawBytes + tj * F::kBytes + (warp >= 12 ? F::kVszOff : F::kKszOff) +
-                              (key & 15) * F::kSzRow;
-          if (!((raw_gone[rs] >> tj) & 1u) && t * kBlockKeys + key < S.nk) {
+        // the block's scales have been looked at, and this warp's two pairs of tiles are there (as they are then)
+        ok = wait_bar(&info_full[blk % kInfos], (blk / kInfos) & 1u, ab);
 #pragma unroll
-            for (int g = 0; g < D / 64; ++g) {
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(sz + 4 * g);
-              const float step = __uint_as_float(w << 16), low = __uint_as_float(w & 0xFFFF0000u);
-              odd = odd || !(fabsf(low) < INFINITY && step < INFINITY);
-              top = fmaxf(top, fmaxf(fabsf(low), fabsf(fmaf(15.f, step, low))));
-            }
-          }
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t mine = pair + 2 * i + (ct >> 7);
+          ok = ok && wait_bar(&raw_full[mine % C::kRawSlots], (mine / C::kRawSlots) & 1u, ab);
         }
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        const uint32_t odds = __ballot_sync(0xffffffffu, odd);
-        if (lane == 0) {
-          wmax[blk & 1u][warp - 8] = top;
-          if (warp >= 12) wodd[blk & 1u][warp - 12] = odds;
-        }
-        // the eight warps meet here once per block, whatever came of their waits, and go on or stop together
-        ok = codes_all(ok);
+        ok = warp_all(ok);
         if (!ok) break;
-        const uint32_t gone01 = raw_gone[pair % C::kRawSlots] | (raw_gone[(pair + 1) % C::kRawSlots] << 2);
-        const uint32_t gone23 = raw_gone[(pair + 2) % C::kRawSlots] | (raw_gone[(pair + 3) % C::kRawSlots] << 2);
-        const uint32_t gone = gone01 | (gone23 << 4);
+        const BlockInfo& bi = info[blk % kInfos];
+        const uint4 known = *reinterpret_cast<const uint4*>(&bi);
 #pragma unroll 1
         for (int v = 0; v < 2 && ok; ++v) {
           const uint32_t item = 2 * blk + v, slot = item % C::kSlots;
-          float most = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) most = fmaxf(most, wmax[blk & 1u][4 * v + k]);
-          int e = most > 0.f ? min(max(exponent_of(most) + 8, -100), 110) : -100;
-          if (v) e = exp_v = max(exp_v, e);
-          const float f = exp2_int(-e);
+          const float f = exp2_int(-(v ? static_cast<int>(known.y) : exponent_of(__uint_as_float(known.x))));
           const int codes_at = ti * F::kBytes + v * F::kVOff + r * F::kRowBytes + 8 * (D / 64) * c;
           const int sz_at = ti * F::kBytes + (v ? F::kVszOff : F::kKszOff) + r * F::kSzRow;
           ok = warp_all(wait_bar(&kv_empty[slot], ((item / C::kSlots) & 1u) ^ 1u, ab));
@@ -658,8 +662,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
             }
             // absent keys are zero; so is a V that is not finite (the rows that see it become NaN by its bit of odd;
             // the others must not see it)
-            const bool zero = ((gone >> (key >> 4)) & 1u) || t * kBlockKeys + key >= S.nk ||
-                              (v && ((wodd[blk & 1u][key >> 5] >> (key & 31)) & 1u));
+            bool zero = t * kBlockKeys + key >= S.nk;
+            if (known.w != 0) zero = zero || ((known.z >> (key >> 4)) & 1u) || (v && ((bi.odd[key >> 5] >> (key & 31)) & 1u));
 #pragma unroll
             for (int g = 0; g < D / 64; ++g) {
               const Scales sc = scales_of(zero ? 0u : sz[g], f);
@@ -668,15 +672,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
               *reinterpret_cast<uint4*>(at + (put_at ^ 16)) = expand(w[(D / 64) + g], sc);
             }
           }
-          if (ct == 0) {
-            if (v) {
-              info[blk & 1u].v_exp = e;
-            } else {
-              info[blk & 1u].k_back = exp2_int(e);
-              info[blk & 1u].gone = gone;
-            }
-          }
-          if (v && ct < 4) info[blk & 1u].odd[ct] = wodd[blk & 1u][ct];
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&kv_full[slot]);
@@ -691,8 +686,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       constexpr uint32_t kIdS = make_idesc(128, 128, 0, false);  // float16, both K-major
       constexpr uint32_t kIdPV = make_idesc(128, D, 0, true);    // V MN-major
       constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row atoms, version, 128-byte swizzle
-      const uint32_t q_lo = ((smem_addr(smem) + C::kQOff) >> 4) | (1u << 16);
-      const uint32_t kv_lo = (smem_addr(smem) + C::kKvOff) >> 4;
+      const uint32_t base_u = __shfl_sync(0xffffffffu, smem_addr(smem), 0), tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = ((base_u + C::kQOff) >> 4) | (1u << 16);
+      const uint32_t kv_lo = (base_u + C::kKvOff) >> 4;
       auto desc = [](uint32_t lo) {
         uint64_t d;
         asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(kDescHi));
@@ -700,8 +696,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       };
       uint32_t blk = 0, n_p = 0, n_q = 0;  // n_p, n_q: bit q is the parity of tile q's next phase
       auto issue_s = [&](int q, uint32_t item) {
-        const uint32_t d = tmem + q * 128, a = q_lo + q * (C::kTileBytes >> 4);
-        const uint32_t b = (kv_lo + (item % C::kSlots) * (C::kTileBytes >> 4)) | (1u << 16);
+        const uint32_t d = tmem_u + q * 128, a = q_lo + q * (C::kTileBytes >> 4);
+        const uint32_t b = (kv_lo + item * (C::kTileBytes >> 4)) | (1u << 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4;
@@ -710,8 +706,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         tc_commit(&s_full[q]);
       };
       auto issue_pv = [&](int q, uint32_t item, bool acc) {
-        const uint32_t d = tmem + C::kOCol + q * D, a = tmem + q * 128;
-        const uint32_t b = (kv_lo + (item % C::kSlots) * (C::kTileBytes >> 4)) | (static_cast<uint32_t>(C::kBoxBytes >> 4) << 16);
+        const uint32_t d = tmem_u + C::kOCol + q * D, a = tmem_u + q * 128;
+        const uint32_t b = (kv_lo + item * (C::kTileBytes >> 4)) | (static_cast<uint32_t>(C::kBoxBytes >> 4) << 16);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_f16_ts(d, a + kk * 8, desc(b + kk * (16 * 128 >> 4)), kIdPV, (acc || kk > 0) ? 1u : 0u);
@@ -720,7 +716,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       Segment S;
       while (ok && take_segment(p, walks[warp], lane, S)) {
         const int tiles = min(ROWS, S.nq * p.G - S.chunk * ROWS) > 128 ? 2 : 1;
-        if (lane == 0) {
+        {
           const int n = S.t1 - S.t0;
           auto wait_item = [&](uint32_t item) { return wait_bar(&kv_full[item % C::kSlots], (item / C::kSlots) & 1u, ab); };
           // turn j = -1 only brings in the first S; turn j: P.V of block j, then S of the next one, for each tile
@@ -740,24 +736,28 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
               }
               if (!ok) break;
               tc_fence_after();
-              if (j >= 0) {
-                issue_pv(q, v_item, j > 0);
-                if (q == tiles - 1) tc_commit(&kv_empty[v_item % C::kSlots]);
+              const uint32_t vb = __shfl_sync(0xffffffffu, v_item % C::kSlots, 0), kb = __shfl_sync(0xffffffffu, k_item % C::kSlots, 0);
+              if (elect_one()) {
+                if (j >= 0) {
+                  issue_pv(q, vb, j > 0);
+                  if (q == tiles - 1) tc_commit(&kv_empty[v_item % C::kSlots]);
+                }
+                if (more) {
+                  issue_s(q, kb);
+                  if (j + 2 == n) tc_commit(&q_empty[q]);
+                  if (q == tiles - 1) tc_commit(&kv_empty[k_item % C::kSlots]);
+                } else {
+                  tc_commit(&o_done[q]);
+                }
               }
-              if (more) {
-                issue_s(q, k_item);
-                if (j + 2 == n) tc_commit(&q_empty[q]);
-                if (q == tiles - 1) tc_commit(&kv_empty[k_item % C::kSlots]);
-              } else {
-                tc_commit(&o_done[q]);
-              }
+              __syncwarp();
             }
           }
           blk += n;
         }
         ok = warp_all(ok);
       }
-      if (lane == 0) {  // every product has completed before tensor memory is given back
+      if (elect_one()) {  // every product has completed before tensor memory is given back
         tc_commit(&drained);
         drain(&drained, 0);
       }
@@ -830,6 +830,59 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
           drain(&raw_full[i % C::kRawSlots], (i / C::kRawSlots) & 1u);
       }
       __syncwarp();
+    } else {
+      // ============================================================== scales of the blocks, ahead of their codes
+      uint32_t blk = 0, pair = 0;
+      bool ok = true;
+      Segment S;
+      while (ok && take_segment(p, walks[warp], lane, S)) {
+        int exp_v = -100;  // of V: the largest so far
+        for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += 4) {
+          // the largest values, 4 keys per lane; a key that is not there, or not finite, counts as zero
+          float top[2] = {0.f, 0.f};
+          uint32_t gone = 0, odds[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t slot = (pair + i) % C::kRawSlots;
+            ok = ok && warp_all(wait_bar(&raw_full[slot], ((pair + i) / C::kRawSlots) & 1u, ab));
+            const uint32_t missing = raw_gone[slot];
+            gone |= missing << (2 * i);
+            const uint8_t* tile = smem + C::kRawOff + slot * C::kRawBytes + (lane >> 4) * F::kBytes + (lane & 15) * F::kSzRow;
+            const bool there = ok && !((missing >> (lane >> 4)) & 1u) && t * kBlockKeys + 32 * i + lane < S.nk;
+            bool odd = false;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int g = 0; g < D / 64; ++g) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + (v ? F::kVszOff : F::kKszOff) + 4 * g);
+                const float step = __uint_as_float(w << 16), low = __uint_as_float(w & 0xFFFF0000u);
+                const bool finite = fabsf(low) < INFINITY && step < INFINITY;
+                if (there && finite) top[v] = fmaxf(top[v], fmaxf(fabsf(low), fabsf(fmaf(15.f, step, low))));
+                if (v) odd = odd || (there && !finite);
+              }
+            odds[i] = __ballot_sync(0xffffffffu, odd);
+          }
+          if (!ok) break;
+          int e[2];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[v])));
+            e[v] = most > 0.f ? min(max(exponent_of(most) + 8, -100), 110) : -100;
+          }
+          exp_v = max(exp_v, e[1]);
+          if (lane == 0) {
+            // read last for block blk - 8, whose tiles the ring has long let go of, and its softmax too: the K of block
+            // blk - 4 came after that block's V had been multiplied
+            BlockInfo& bi = info[blk % kInfos];
+            bi.k_back = exp2_int(e[0]), bi.v_exp = exp_v, bi.gone = gone;
+            bi.special = gone | odds[0] | odds[1] | odds[2] | odds[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bi.odd[i] = odds[i];
+            bar_arrive(&info_full[blk % kInfos]);
+          }
+          __syncwarp();
+        }
+      }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
