@@ -147,9 +147,10 @@ unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total
  *               tokens are the last ones); 0: every key.  A row with no key gets O = 0, LSE = -inf.
  *   workspace   attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, 0) bytes, 16-byte aligned, overwritten; not shared by calls
  *               that may run at the same time.
- * Arithmetic: scores from exact products of the codes with Q in float16 (each row scaled by a power of two so
- * that its largest entry keeps all its bits; without the transform bf16 entries are exact over 2^-24 of it),
- * summed in float32; softmax in float32; P times the step of V rounded to float16, summed in float32.
+ * Arithmetic: softmax and sums in float32.  Requests of few rows (queries times Hq / Hk; up to 64 at d = 64, 48 at
+ * d = 128, any number at d = 256): the codes are multiplied as they are, Q in 22 bits (each row scaled by a power
+ * of two), P times the step of V rounded to float16.  Others: Q (transformed), K, V and P rounded to float16 under
+ * powers of two of their rows and blocks, so a score is off by 2^-10 of the sum of its products' sizes.
  * Work is split over keys by a rule on the lengths, and the parts are joined in a fixed order: results do
  * not depend on scheduling.  Offsets or lengths that break their rules skip that request (its rows are not
  * written), and a table entry outside the cache leaves its keys out; both are reported by

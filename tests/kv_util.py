@@ -66,9 +66,9 @@ def reference(q, ks, vs, cu, ctx, scale, causal, signs=None):
                              None if signs is None else signs.cpu().numpy())
 
 
-# Requests with more rows (queries times heads per key/value head) than this, at d <= 128, go to the kernel
-# that brings K and V to float16
-FEW_ROWS = 32
+# Requests with more rows (queries times heads per key/value head) than this go to the kernel that brings K and V to
+# float16
+FEW_ROWS = {64: 64, 128: 48, 256: 2 ** 31}
 
 
 def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
@@ -81,20 +81,20 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     whose codes carry an offset, at most 16 times the value's own size, cut off at 2^-23 each), x = 2^-20; p_j times
     V's step is rounded by 2^-11, which moves O by 2^-11 sum_j p_j (|v_j| + 15 s_j) <= 2^-11 3 sum_j p_j max|v_j| (a code
     times its step is at most the range, twice the largest value).
-    Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18; the exponential of a quarter
-    of the keys is a cubic, off by 7.5e-5: x = 8e-5; V is rounded by 2^-11, p too, twice where the maximum moved:
-    3 2^-11 sum_j p_j |v_j|.
+    Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18, x as above; V is rounded by
+    2^-11, p too, twice where the maximum moved: 3 2^-11 sum_j p_j |v_j|.
     O is rounded to bf16, 2^-8.  Second order: the whole times 1.1."""
     q = q.float().cpu().numpy().astype(np.float64)
     if signs is not None:
         q = hadamard_f64(q, signs.cpu().numpy())
     ob, lb = np.full(o_ref.shape, np.inf), np.full(lse_ref.shape, np.inf)
     group = q.shape[1] // ks[0].shape[1]
+    few = FEW_ROWS[q.shape[2]]
     most = max((int(cu[b + 1]) - int(cu[b])) * group for b in range(len(ctx)))
     for b, n in enumerate(ctx):
         lo, hi = int(cu[b]), int(cu[b + 1])
-        many = q.shape[2] <= 128 and most > FEW_ROWS and ((hi - lo) * group > FEW_ROWS or len(ctx) == 1)
-        e, x = (2.0 ** -10 + 2.0 ** -18, 8e-5) if many else (2.0 ** -21 + 2.0 ** -18, 2.0 ** -20)
+        many = most > few and ((hi - lo) * group > few or len(ctx) == 1)
+        e, x = (2.0 ** -10 if many else 2.0 ** -21) + 2.0 ** -18, 2.0 ** -20
         for h in range(q.shape[1]):
             kh = h // group
             for i in range(lo, hi):

@@ -28,6 +28,11 @@ def test_matches_the_oracle(d, transform, ctx, nq, Hq, Hk, page):
     _run(ctx, nq, Hq, Hk, d, page, True, transform, seed=sum(ctx) + d)
 
 
+@pytest.mark.parametrize("d,rows", [(64, 64), (64, 66), (128, 48), (128, 50)])
+def test_requests_on_both_sides_of_the_choice_of_kernel(d, rows):
+    _run([rows, 210, 77], [rows // 2, rows // 2, 1], 4, 2, d, 16, True, True, seed=rows)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_without_the_causal_mask(d):
     _run([333, 1], [150, 40], 4, 2, d, 16, causal=False, transform=True, seed=d)
