@@ -45,57 +45,53 @@ def declare(L) -> None:
 
 
 # A decode step calls each of these once per layer for a few microseconds of GPU work, so the checks
-# below are written to cost little: one look at the current device per call, plain attribute
-# comparisons per tensor, integers handed to ctypes.
+# below are written to cost little: one look at the current device per call, each property of a tensor asked for
+# once, plain comparisons, integers handed to ctypes.
+
+def _refuse_device(t, what):
+    raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+
 
 def _arg(t, shape, dtype, what, dev):
     """Address of a contiguous tensor of this shape and type on the current device."""
     if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, contiguous")
     if t.get_device() != dev:
-        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+        _refuse_device(t, what)
     return t.data_ptr()
 
 
 def _rows(t, shape, dtypes, what, dev):
-    """Address of a tensor whose last dimension is contiguous, the others by their strides."""
-    if t.shape != shape or t.dtype not in dtypes or t.stride(-1) != 1:
+    """Strides and address of a tensor whose last dimension is contiguous.  ``shape`` None: any."""
+    strides = t.stride()
+    if (shape is not None and t.shape != shape) or t.dtype not in dtypes or strides[-1] != 1:
         names = "/".join(str(x).replace("torch.", "") for x in dtypes)
-        raise ValueError(f"{what} must be {names} of shape {tuple(shape)} with a contiguous last dimension")
+        raise ValueError(f"{what} must be {names} of shape {tuple(shape or t.shape)} with a contiguous last dimension")
     if t.get_device() != dev:
-        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+        _refuse_device(t, what)
+    return strides, t.data_ptr()
 
 
-def _device(torch, *tensors):
-    """The current CUDA device; host tensors are refused before CUDA is asked for it."""
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError(f"a {tuple(t.shape)} tensor is on {t.device}, not on the current CUDA device")
-    return torch.cuda.current_device()
+def _device(torch, t):
+    """The current CUDA device; a host tensor is refused before CUDA is asked for it."""
+    if not t.is_cuda:
+        raise ValueError(f"a {tuple(t.shape)} tensor is on {t.device}, not on the current CUDA device")
+    return torch._C._cuda_getDevice()
 
 
-def _on_stream(f):
-    """With ``stream``: runs the call with that stream current, so that the tensors it makes belong to it."""
-    import functools
-
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        import torch
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+def _again(f, stream, *args):
+    """The call with ``stream`` current, so that the tensors it makes belong to it."""
+    import torch
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def _raw_stream(torch, dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-@_on_stream
 def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, total, slots=None, positions=None,
-                   cu_seqlens=None, lens_out=None, cursor_out=None):
+                   cu_seqlens=None, lens_out=None, cursor_out=None, stream=None):
     """Block tables and slot maps of one serving step, on the GPU.
 
     ``lens``, ``new_lens`` [B] int32: tokens each request holds, and adds now; ``block_table``
@@ -105,10 +101,13 @@ def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, 
     ``lens_out=lens`` and ``cursor_out=cursor`` update in place.  A request for which the free blocks do
     not suffice is not served: its slots are -1 and its length stays.
     """
+    if stream is not None:
+        return _again(attn_kv_tables, stream, lens, new_lens, block_table, free_blocks, cursor, page_size, total, slots,
+                      positions, cu_seqlens, lens_out, cursor_out)
     import torch
     if lens.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1 or lens.shape[0] == 0:
         raise ValueError("expected lens [B], block_table [B, width], free_blocks [n]")
-    B, width, n_free, total = lens.shape[0], block_table.shape[1], free_blocks.shape[0], int(total)
+    (B,), (_, width), (n_free,), total = lens.shape, block_table.shape, free_blocks.shape, int(total)
     if total < 0:
         raise ValueError("total must not be negative")
     dev, i32 = _device(torch, lens), torch.int32
@@ -118,7 +117,7 @@ def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, 
     if slots is None and positions is None and cu_seqlens is None and lens_out is None and cursor_out is None:
         # one allocation for the five
         room = lens.new_empty(2 * total + 2 * B + 2)
-        slots, positions, cu_seqlens, lens_out, cursor_out = room.split((total, total, B + 1, B, 1))
+        slots, positions, cu_seqlens, lens_out, cursor_out = room.split_with_sizes((total, total, B + 1, B, 1))
         at = room.data_ptr()
         outs = (at, at + 4 * total, at + 8 * total, at + 8 * total + 4 * B + 4, at + 8 * total + 8 * B + 4)
     else:
@@ -135,59 +134,70 @@ def attn_kv_tables(lens, new_lens, block_table, free_blocks, cursor, page_size, 
     return slots, positions, cu_seqlens, lens_out, cursor_out, block_table
 
 
-def _dims(t):
+def _dims(t, strides):
     """(B, heads, N, d) and (batch, head, row) strides of [tokens, heads, d] or [B, heads, N, d]."""
     if t.dim() == 3:
-        (n, h, d), (sn, sh, _) = t.shape, t.stride()
-        return (1, h, n, d), (8, sh, sn)
-    return tuple(t.shape), t.stride()[:3]
+        n, h, d = t.shape
+        return (1, h, n, d), (8, strides[1], strides[0])
+    return tuple(t.shape), strides[:3]
+
+
+# sum of the sections and their C array (read only) by the sections
+_sections = {}
 
 
 def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse, name):
     import torch
     f32 = torch.float32
     types = (torch.bfloat16, f32)
-    half = sum(sections)
+    sections = tuple(sections)
+    known = _sections.get(sections)
+    if known is None:
+        if len(_sections) >= 256:
+            _sections.clear()
+        known = _sections[sections] = sum(sections), (ctypes.c_int * len(sections))(*sections)
+    half, c_sections = known
     if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
         raise ValueError("q and k must be [tokens, heads, d] or [B, heads, N, d]")
     if cos.dim() != 2 or cos.shape[0] == 0:
         raise ValueError("cos and sin must be float32 [n_pos, sum of the sections]")
     dev = _device(torch, q)
-    (B, Hq, N, d), strides_q = _dims(q)
-    pq = _rows(q, q.shape, types, "q", dev)
-    tables = _arg(cos, (cos.shape[0], half), f32, "cos", dev), _arg(sin, (cos.shape[0], half), f32, "sin", dev)
+    strides, pq = _rows(q, None, types, "q", dev)
+    (B, Hq, N, d), strides_q = _dims(q, strides)
+    shape = (cos.shape[0], half)
+    pc, ps = _arg(cos, shape, f32, "cos", dev), _arg(sin, shape, f32, "sin", dev)
     if positions.dim() == 1 and q.dim() == 3 and len(sections) == 1:
         positions = positions[None]
     at = _arg(positions, (len(sections), N) if q.dim() == 3 else (len(sections), B, N), torch.int32, "positions", dev)
     out_dtype = out_dtype or (q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else q.dtype)
     if q_out is None:
         q_out = torch.empty_like(q, dtype=out_dtype)
-    pqo = _rows(q_out, q.shape, types, "q_out", dev)
+    strides, pqo = _rows(q_out, q.shape, types, "q_out", dev)
+    strides_qo = _dims(q_out, strides)[1]
     strides_k = strides_ko = (8, 8, 8)
     Hk = pk = pko = 0
     if k is not None:
-        (Bk, Hk, Nk, dk), strides_k = _dims(k)
-        if (Bk, Nk, dk) != (B, N, d):
+        strides, pk = _rows(k, None, (q.dtype,), "k", dev)
+        (Bk, Hk, Nk, dk), strides_k = _dims(k, strides)
+        if Bk != B or Nk != N or dk != d:
             raise ValueError("k must have q's tokens and d")
-        pk = _rows(k, k.shape, (q.dtype,), "k", dev)
         if k_out is None:
             k_out = torch.empty_like(k, dtype=q_out.dtype)
-        pko = _rows(k_out, k.shape, (q_out.dtype,), "k_out", dev)
-        strides_ko = _dims(k_out)[1]
+        strides, pko = _rows(k_out, k.shape, (q_out.dtype,), "k_out", dev)
+        strides_ko = _dims(k_out, strides)[1]
     elif k_out is not None:
         raise ValueError("k_out without k")
     if B == 0 or N == 0:
         return q_out, k_out
-    _check(lib().attn_rope_axes(pq, pk, pqo, pko, *tables, at, B, Hq, Hk, N, d, len(sections),
-                                (ctypes.c_int * len(sections))(*sections), cos.shape[0],
-                                _LL12(*strides_q, *strides_k, *_dims(q_out)[1], *strides_ko), inverse,
+    _check(lib().attn_rope_axes(pq, pk, pqo, pko, pc, ps, at, B, Hq, Hk, N, d, len(sections),
+                                c_sections, cos.shape[0],
+                                _LL12(*strides_q, *strides_k, *strides_qo, *strides_ko), inverse,
                                 ATTN_FP32 if q.dtype is f32 else ATTN_BF16, ATTN_FP32 if q_out.dtype is f32 else ATTN_BF16,
                                 _raw_stream(torch, dev)), name)
     return q_out, k_out
 
 
-@_on_stream
-def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, out_dtype=None):
+def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, out_dtype=None, stream=None):
     """Rotary embedding of ``q`` and ``k`` (``k`` may be None) with one to four position axes.
 
     ``q``, ``k``: [tokens, heads, d] or [B, heads, N, d], bf16 or float32, last dimension contiguous;
@@ -195,13 +205,16 @@ def attn_rope_axes(q, k, cos, sin, positions, sections, q_out=None, k_out=None, 
     ``positions`` int32 [axes, tokens] or [axes, B, N]; ``sections``: how many of the ``half`` pairs turn
     with each axis, in order.  Coordinates i and i + half form pair i; dimensions past 2 * half are
     copied.  ``q_out=q``, ``k_out=k`` rotate in place.  Returns ``(q_out, k_out)``."""
+    if stream is not None:
+        return _again(attn_rope_axes, stream, q, k, cos, sin, positions, sections, q_out, k_out, out_dtype)
     return _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, 0, "attn_rope_axes")
 
 
-@_on_stream
-def attn_rope_axes_bwd(dq, dk, cos, sin, positions, sections, dq_out=None, dk_out=None, out_dtype=None):
+def attn_rope_axes_bwd(dq, dk, cos, sin, positions, sections, dq_out=None, dk_out=None, out_dtype=None, stream=None):
     """The backward of :func:`attn_rope_axes`: gradients of its outputs to gradients of its inputs
     (bf16 or float32 each), with the same tables, positions and sections."""
+    if stream is not None:
+        return _again(attn_rope_axes_bwd, stream, dq, dk, cos, sin, positions, sections, dq_out, dk_out, out_dtype)
     return _rope(dq, dk, cos, sin, positions, sections, dq_out, dk_out, out_dtype, 1, "attn_rope_axes_bwd")
 
 
@@ -217,39 +230,46 @@ def attn_kv4_cache(num_blocks, Hk, page_size, d, device=None):
 
 def _cache_dims(cache, torch, dev):
     """(num_blocks, Hk, page_size, d) of a cache, and its address."""
-    if cache.dim() != 4 or cache.shape[3] % 18:
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be contiguous uint8 [num_blocks, Hk, page / 16, 18 d]")
-    nb, hk, tiles, tile = cache.shape
-    return nb, hk, 16 * tiles, tile // 18, _arg(cache, cache.shape, torch.uint8, "cache", dev)
+    nb, hk, tiles, tile = shape
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous uint8 [num_blocks, Hk, page / 16, 18 d]")
+    if cache.get_device() != dev:
+        _refuse_device(cache, "cache")
+    return nb, hk, 16 * tiles, tile // 18, cache.data_ptr()
 
 
 def _sign_arg(signs, d, torch, dev):
     return _arg(signs, (d,), torch.int8, "signs", dev) if signs is not None else 0
 
 
-@_on_stream
-def attn_kv4_append(k, v, cache, slots, signs=None):
+def attn_kv4_append(k, v, cache, slots, signs=None, stream=None):
     """Quantises ``k``, ``v`` [T, Hk, d] bf16 (row and head strides free) to 4 bits and writes them to
     ``slots`` [T] int32 of ``cache``, in place (slot -1: skipped).  ``signs`` (d int8 entries +-1) puts
     K through the random-sign Hadamard transform first; give the same to :func:`attn_fwd_kv4`.
     Returns ``cache``."""
+    if stream is not None:
+        return _again(attn_kv4_append, stream, k, v, cache, slots, signs)
     import torch
     dev, bf16 = _device(torch, k), (torch.bfloat16,)
     nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
     T = k.shape[0]
-    pk, pv = _rows(k, (T, Hk, d), bf16, "k", dev), _rows(v, (T, Hk, d), bf16, "v", dev)
+    ((kn, kh, _), pk), ((vn, vh, _), pv) = _rows(k, (T, Hk, d), bf16, "k", dev), _rows(v, (T, Hk, d), bf16, "v", dev)
     ps, pg = _arg(slots, (T,), torch.int32, "slots", dev), _sign_arg(signs, d, torch, dev)
     if T:
-        _check(lib().attn_kv4_append(pk, pv, pc, ps, pg, T, Hk, d, page, nb, _LL4(*k.stride()[:2], *v.stride()[:2]),
+        _check(lib().attn_kv4_append(pk, pv, pc, ps, pg, T, Hk, d, page, nb, _LL4(kn, kh, vn, vh),
                                      _raw_stream(torch, dev)), "attn_kv4_append")
     return cache
 
 
-@_on_stream
-def attn_kv4_read(cache, slots, k=None, v=None, dtype=None):
+def attn_kv4_read(cache, slots, k=None, v=None, dtype=None, stream=None):
     """The values held at ``slots`` [T] int32 of ``cache``: ``(k, v)`` [T, Hk, d] in ``dtype``
     (torch.bfloat16, the default, or torch.float32); slot -1 gives zeros.  A K that was transformed comes
     back transformed."""
+    if stream is not None:
+        return _again(attn_kv4_read, stream, cache, slots, k, v, dtype)
     import torch
     dev = _device(torch, cache)
     nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
@@ -266,7 +286,7 @@ def attn_kv4_read(cache, slots, k=None, v=None, dtype=None):
     else:
         pk = _arg(k, (T, Hk, d), dt, "k", dev)
     if v is None:
-        v = cache.new_empty((T, Hk, d), dtype=dt)
+        v = torch.empty_like(k, memory_format=torch.contiguous_format)
         pv = v.data_ptr()
     else:
         pv = _arg(v, (T, Hk, d), dt, "v", dev)
@@ -287,9 +307,8 @@ def attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, num_sms=0)
 _workspace_bytes = {}
 
 
-@_on_stream
 def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_q=1, o=None, lse=None, workspace=None,
-                 signs=None, scale=None, causal=True, want_lse=True):
+                 signs=None, scale=None, causal=True, want_lse=True, stream=None):
     """Attention of ``q`` [total_q, Hq, d] bf16 (row and head strides free) over the 4-bit ``cache``,
     query head h reading key/value head ``h // (Hq // Hk)``.
 
@@ -300,16 +319,20 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
     Rows that see no key get O = 0, LSE = -inf.  Returns ``(o [total_q, Hq, d] bf16, lse [Hq, total_q]
     float32)``; rows behind the last request are left as they were.
     """
+    if stream is not None:
+        return _again(attn_fwd_kv4, stream, q, cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, o, lse, workspace,
+                      signs, scale, causal, want_lse)
     import torch
     dev, i32, bf16 = _device(torch, q), torch.int32, (torch.bfloat16,)
     nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
-    if q.dim() != 3 or q.shape[2] != d or q.shape[1] % Hk:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d or shape[1] % Hk:
         raise ValueError("q must be [total_q, Hq, d] with the cache's d and a multiple of its heads")
     if block_table.dim() != 2 or block_table.shape[0] == 0:
         raise ValueError("block_table must be [B, width]")
-    total_q, Hq, _ = q.shape
+    total_q, Hq, _ = shape
     B, width = block_table.shape
-    pq = _rows(q, q.shape, bf16, "q", dev)
+    (qn, qh, _), pq = _rows(q, None, bf16, "q", dev)
     pt = _arg(block_table, (B, width), i32, "block_table", dev)
     pl = _arg(seq_lens, (B,), i32, "seq_lens", dev)
     pcu = 0
@@ -319,10 +342,10 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
         raise ValueError("without cu_seqlens_q there is one query per request")
     pg = _sign_arg(signs, d, torch, dev)
     if o is None:
-        o = q.new_empty((total_q, Hq, d))
-        po, so = o.data_ptr(), (Hq * d, d)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        on, oh, po = Hq * d, d, o.data_ptr()
     else:
-        po, so = _rows(o, (total_q, Hq, d), bf16, "o", dev), o.stride()[:2]
+        (on, oh, _), po = _rows(o, shape, bf16, "o", dev)
     pe = 0
     if lse is not None:
         pe = _arg(lse, (Hq, total_q), torch.float32, "lse", dev)
@@ -339,13 +362,13 @@ def attn_fwd_kv4(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_
             _workspace_bytes.clear()
         nbytes = _workspace_bytes[sizes] = L.attn_fwd_kv4_workspace_bytes(*sizes[:6], 0)
     if workspace is None:
-        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+        workspace = cache.new_empty(nbytes)
         pw = workspace.data_ptr()
     else:
         if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"attn_fwd_kv4: the workspace must be contiguous and have {nbytes} bytes")
         pw = _arg(workspace, workspace.shape, workspace.dtype, "workspace", dev)
     _check(L.attn_fwd_kv4(pq, pc, pt, pl, pcu, po, pe, pw, pg, B, Hq, Hk, total_q, max_seqlen_q, d, page, nb, width,
-                          _LL4(*q.stride()[:2], *so), float(scale) if scale is not None else 1.0 / math.sqrt(d),
+                          _LL4(qn, qh, on, oh), float(scale) if scale is not None else 1.0 / math.sqrt(d),
                           1 if causal else 0, _raw_stream(torch, dev)), "attn_fwd_kv4")
     return o, lse
