@@ -6,12 +6,13 @@
 // bf16 >= (max y - z) / 15, u = rint((y - z) / s).  Rounding z down and s up keeps every value within
 // z .. z + 15 s, so no code is cut off by the rounding of its own scale.
 //
-// Bound by memory: 4 bytes of K and V read and 1.125 written per value pair.  A lane holds 16
-// consecutive values of a row (two 16-byte loads, d / 16 lanes per row, several rows per warp), so four of
-// the transform's stages and most of the minimum and maximum stay in the lane, and a group is four
-// adjacent lanes.  K and V rows go to different blocks of threads.  The quotients come from the group's one
-// reciprocal, corrected to the rounded quotient (three operations instead of a division each: 54 us before for
-// 16,384 tokens of 8 heads of 128).
+// Append has 4 bytes to read and 1.125 to write per value pair (13 us for 16,384 tokens of 8 heads of 128), and is bound
+// by its instructions, 28.6 us: a lane holds 16 consecutive values of a row (two 16-byte loads, d / 16 lanes per
+// row, several rows per warp), so four of the transform's stages and most of the minimum and maximum stay in the
+// lane, and a group is four adjacent lanes.  K and V rows go to different blocks of threads.  The quotients come from the
+// group's one reciprocal, corrected to the rounded quotient (three operations instead of a division each: 54 us
+// before), each row's addresses from one lane instead of its d / 16, and a round's values are asked for while the
+// one before is worked on.
 //
 // Read: a thread has four dimensions of a row, so that each store of a warp is contiguous.
 
@@ -49,126 +50,159 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Rounds of a warp of the writer, up to 4 where there are enough rows for 4 blocks of threads on each of 148 processors
+// all the same (16,384 tokens of 8 heads of 128: 39.6, 32.1 and 28.6 us with 1, 2 and 4).
+constexpr int kAppendRounds = 4;
+constexpr long long kAppendBlocks = 4 * 148;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CacheParams p) {
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4CacheParams p, const int rounds) {
   using F = Kv4Tile<D>;
-  constexpr int kLanes = D / 16;  // lanes per row
+  constexpr int kLanes = D / 16;         // lanes per row
+  constexpr int kAtOnce = 32 / kLanes;   // rows of a warp
   const int lane = threadIdx.x & 31;
   const int j = lane % kLanes;
   const bool is_v = blockIdx.y != 0;
   const bool transform = !is_v && p.signs != nullptr;
-  // fewer than 2^31 rows (the caller's bound), and a block of threads past them at most
-  const unsigned row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  int t = 0, h = 0, slot = -1;
-  if (row < static_cast<unsigned>(p.T) * static_cast<unsigned>(p.Hk)) {
-    t = static_cast<int>(row / static_cast<unsigned>(p.Hk));
-    h = static_cast<int>(row) - t * p.Hk;
-    slot = p.slots[t];
+  // Lane i finds where row first + i comes from and goes to, for the whole warp (fewer than 2^31 rows, the caller's bound,
+  // and a block's rows past them at most).  `to`: its row in the tile in the upper 8 bits, all ones: nowhere.
+  const unsigned rows = static_cast<unsigned>(p.T) * static_cast<unsigned>(p.Hk);
+  const unsigned first = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * (rounds * kAtOnce);
+  long long from = 0;
+  unsigned long long to = ~0ull;
+  if (lane < rounds * kAtOnce && first + lane < rows) {
+    const unsigned row = first + lane;
+    const int t = static_cast<int>(row / static_cast<unsigned>(p.Hk)), h = static_cast<int>(row) - t * p.Hk;
+    const int slot = p.slots[t];
+    from = t * (is_v ? p.v_sn : p.k_sn) + h * (is_v ? p.v_sh : p.k_sh);
+    const int block = slot < 0 ? 0 : slot / p.page, off = slot - block * p.page;
+    if (slot < -1 || block >= p.num_blocks) atomicOr(p.status, kDevStatusBadSeqlens);
+    else if (slot >= 0)
+      to = static_cast<unsigned long long>(kv4_tile_offset<D>(block, off, p.page, p.Hk, h)) |
+           (static_cast<unsigned long long>(off & 15) << 56);
   }
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  if (slot >= 0) {
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
-                               t * (is_v ? p.v_sn : p.k_sn) + h * (is_v ? p.v_sh : p.k_sh) + 16 * j;
-    const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  if (transform) {  // uniform over the block
+  uint32_t flip[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // the sign bits of this lane's pairs
+  if (transform) {
     const int4 sg = *reinterpret_cast<const int4*>(p.signs + 16 * j);
     const int sw[4] = {sg.x, sg.y, sg.z, sg.w};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (static_cast<signed char>(sw[i >> 2] >> (8 * (i & 3))) == -1) x[i] = -x[i];
-#pragma unroll
-    for (int s = 1; s < 16; s <<= 1)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (!(i & s)) {
-          const float a = x[i], b = x[i | s];
-          x[i] = a + b;
-          x[i | s] = a - b;
-        }
-#pragma unroll
-    for (int s = 1; s < kLanes; s <<= 1) {
-      const float sign = (j & s) ? -1.f : 1.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)  // other + x, or other - x: the product is exact
-        x[i] = fmaf(sign, x[i], __shfl_xor_sync(0xffffffffu, x[i], s));
+      if (static_cast<signed char>(sw[i >> 2] >> (8 * (i & 3))) == -1) flip[i >> 1] |= i & 1 ? 0x80000000u : 0x8000u;
+  }
+  const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) + 16 * j;
+  uint4 na = make_uint4(0u, 0u, 0u, 0u), nb = na;
+  auto ask = [&](int k) {  // for the values of round k
+    const int of = k * kAtOnce + lane / kLanes;
+    const long long at = __shfl_sync(0xffffffffu, from, of);
+    if (first + of < rows) {
+      na = reinterpret_cast<const uint4*>(src + at)[0];
+      nb = reinterpret_cast<const uint4*>(src + at)[1];
     }
-    constexpr float kNorm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], kNorm);
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
-#pragma unroll
-  for (int s = 1; s < 4; s <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-  }
-  float z = bf16_down(lo);
-  const float range = __fsub_rn(hi, z);
-  // a NaN goes through the minimum and the maximum, an infinity makes the range infinite or NaN
-  const unsigned odds = __ballot_sync(0xffffffffu, !isfinite(range));
-  float s = bf16_up(__fdiv_rn(range, 15.f));
-  uint32_t code[2] = {0u, 0u};
-  if ((odds >> (lane & ~3)) & 15u) {
-    s = z = __uint_as_float(0x7FC00000u);
-  } else if (s > 1e-30f && s < 1e30f) {
-    // With y = 1 / s rounded, q = t y and the exact remainder t - q s, q + remainder y is the rounded quotient (Markstein).
-    // It is at least 0 and rounds to 15 at most; 1.5 2^23 added rounds it to the nearest integer, in the low bits.
-    const float y = __frcp_rn(s);
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t c = 0u;
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        const float u = __fsub_rn(x[8 * w + i], z);
-        const float q = __fmul_rn(u, y);
-        const float n = __fadd_rn(fmaf(fmaf(-q, s, u), y, q), 12582912.f);
-        c = c * 16u + __float_as_uint(n);
-      }
-      code[w] = c - 0x11111111u * 0x4B400000u;  // what the shift's own bits add up to
-    }
-  } else if (s > 0.f) {
+  };
+  ask(0);
 #pragma unroll 1
-    for (int w = 0; w < 2; ++w)
+  for (int k = 0; k < rounds; ++k) {
+    const unsigned long long dst = __shfl_sync(0xffffffffu, to, k * kAtOnce + lane / kLanes);
+    float x[16];
+    {
+      const uint32_t w[8] = {na.x, na.y, na.z, na.w, nb.x, nb.y, nb.z, nb.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(w ? x[8 + i] : x[i], z), s)), 0.f), 15.f);
-        code[w] |= static_cast<uint32_t>(u) << (4 * i);
+        const uint32_t u = w[i] ^ flip[i];
+        x[2 * i] = __uint_as_float(u << 16);
+        x[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
       }
+    }
+    if (k + 1 < rounds) ask(k + 1);
+    if (transform) {  // uniform over the block
+#pragma unroll
+      for (int s = 1; s < 16; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(i & s)) {
+            const float a = x[i], b = x[i | s];
+            x[i] = a + b;
+            x[i | s] = a - b;
+          }
+#pragma unroll
+      for (int s = 1; s < kLanes; s <<= 1) {
+        const float sign = (j & s) ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // other + x, or other - x: the product is exact
+          x[i] = fmaf(sign, x[i], __shfl_xor_sync(0xffffffffu, x[i], s));
+      }
+      constexpr float kNorm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], kNorm);
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) {
+      lo = min_nan(lo, x[i]);
+      hi = max_nan(hi, x[i]);
+    }
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+    }
+    float z = bf16_down(lo);
+    const float range = __fsub_rn(hi, z);
+    // a NaN goes through the minimum and the maximum, an infinity makes the range infinite or NaN
+    const unsigned odds = __ballot_sync(0xffffffffu, !isfinite(range));
+    // range / 15 rounded, likewise
+    float s;
+    if (range > 1e-28f && range < 1e30f) {
+      constexpr float kY = 1.f / 15.f;
+      const float q = __fmul_rn(range, kY);
+      s = bf16_up(fmaf(fmaf(-q, 15.f, range), kY, q));
+    } else {
+      s = bf16_up(__fdiv_rn(range, 15.f));
+    }
+    uint32_t code[2] = {0u, 0u};
+    if ((odds >> (lane & ~3)) & 15u) {
+      s = z = __uint_as_float(0x7FC00000u);
+    } else if (s > 1e-30f && s < 1e30f) {
+      // With y = 1 / s rounded, q = t y and the exact remainder t - q s, q + remainder y is the rounded quotient (Markstein).
+      // It is at least 0 and rounds to 15 at most; 1.5 2^23 added rounds it to the nearest integer, in the low bits.
+      const float y = __frcp_rn(s);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t c = 0u;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const float u = __fsub_rn(x[8 * w + i], z);
+          const float q = __fmul_rn(u, y);
+          const float n = __fadd_rn(fmaf(fmaf(-q, s, u), y, q), 12582912.f);
+          c = c * 16u + __float_as_uint(n);
+        }
+        code[w] = c - 0x11111111u * 0x4B400000u;  // what the shift's own bits add up to
+      }
+    } else if (s > 0.f) {
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(w ? x[8 + i] : x[i], z), s)), 0.f), 15.f);
+          code[w] |= static_cast<uint32_t>(u) << (4 * i);
+        }
+    }
+    if (dst == ~0ull) continue;
+    uint8_t* tile = p.cache + (dst & ((1ull << 56) - 1));
+    const int r = static_cast<int>(dst >> 56);
+    const int plane = j / (F::kPlaneDims / 16), g = (j / 4) % F::kGroups, c = j & 3;  // dims 64 g + 16 c .. of the plane
+    if (!is_v) {
+      *reinterpret_cast<uint2*>(tile + plane * F::kPlaneBytes + r * F::kRowBytes + c * 8 * F::kGroups + 8 * g) =
+          make_uint2(code[0], code[1]);
+    } else {
+      uint8_t* d = tile + F::kVOff + plane * F::kPlaneBytes + r * F::kRowBytes + 2 * c * 4 * F::kGroups + 4 * g;
+      *reinterpret_cast<uint32_t*>(d) = code[0];
+      *reinterpret_cast<uint32_t*>(d + 4 * F::kGroups) = code[1];
+    }
+    if (c == 0)
+      *reinterpret_cast<uint32_t*>(tile + (is_v ? F::kVszOff : F::kKszOff) + r * F::kSzRow + 4 * (j / 4)) =
+          (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xFFFF0000u);
   }
-  if (slot == -1) return;
-  const int block = slot / p.page, off = slot - block * p.page;
-  if (slot < 0 || block >= p.num_blocks) {
-    atomicOr(p.status, kDevStatusBadSeqlens);
-    return;
-  }
-  uint8_t* tile = p.cache + kv4_tile_offset<D>(block, off, p.page, p.Hk, h);
-  const int r = off & 15;
-  const int plane = j / (F::kPlaneDims / 16), g = (j / 4) % F::kGroups, c = j & 3;  // dims 64 g + 16 c .. of the plane
-  if (!is_v) {
-    *reinterpret_cast<uint2*>(tile + plane * F::kPlaneBytes + r * F::kRowBytes + c * 8 * F::kGroups + 8 * g) =
-        make_uint2(code[0], code[1]);
-  } else {
-    uint8_t* d = tile + F::kVOff + plane * F::kPlaneBytes + r * F::kRowBytes + 2 * c * 4 * F::kGroups + 4 * g;
-    *reinterpret_cast<uint32_t*>(d) = code[0];
-    *reinterpret_cast<uint32_t*>(d + 4 * F::kGroups) = code[1];
-  }
-  if (c == 0)
-    *reinterpret_cast<uint32_t*>(tile + (is_v ? F::kVszOff : F::kKszOff) + r * F::kSzRow + 4 * (j / 4)) =
-        (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xFFFF0000u);
 }
 
 // One store of a warp: half a row of d = 256, a row of 128, two of 64.  A warp has kReadRows such rows (or pairs), whose
@@ -251,10 +285,13 @@ dim3 grid_of(const Kv4CacheParams& p, int rows_per_block) {
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4CacheParams& p, int d, cudaStream_t stream) {
-  const dim3 grid = grid_of(p, kThreads / (d / 16));
-  if (d == 64) kv4_append_kernel<64><<<grid, kThreads, 0, stream>>>(p);
-  else if (d == 128) kv4_append_kernel<128><<<grid, kThreads, 0, stream>>>(p);
-  else kv4_append_kernel<256><<<grid, kThreads, 0, stream>>>(p);
+  const int step = kThreads / (d / 16);
+  const long long full = static_cast<long long>(p.T) * p.Hk / (kAppendBlocks * step);
+  const int rounds = full < 1 ? 1 : full > kAppendRounds ? kAppendRounds : static_cast<int>(full);
+  const dim3 grid = grid_of(p, rounds * step);
+  if (d == 64) kv4_append_kernel<64><<<grid, kThreads, 0, stream>>>(p, rounds);
+  else if (d == 128) kv4_append_kernel<128><<<grid, kThreads, 0, stream>>>(p, rounds);
+  else kv4_append_kernel<256><<<grid, kThreads, 0, stream>>>(p, rounds);
   return cudaGetLastError();
 }
 

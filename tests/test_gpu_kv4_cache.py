@@ -71,6 +71,27 @@ def test_strided_views_of_a_fused_projection():
     assert torch.equal(ea.attn_kv4_read(one, slots)[0][:, 0], ea.attn_kv4_read(a, slots)[0][:, 0])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_tokens_at_once(d):
+    """As many rows as make a thread take several of them, the last ones ragged: the same as in small calls."""
+    T, Hk, page = 20011, 4, 64
+    wide = _kv(d, T, Hk + 1, d, 3.0)
+    k, v = wide[0][:, 1:], wide[1][:, :Hk]
+    signs = torch.from_numpy(hadamard_signs(d)).cuda()
+    slots = np.random.default_rng(d).permutation((T // page + 3) * page)[:T]
+    slots[::17] = -1
+    a, b = ea.attn_kv4_cache(T // page + 3, Hk, page, d), ea.attn_kv4_cache(T // page + 3, Hk, page, d)
+    ea.attn_kv4_append(k, v, a, i32(slots), signs=signs)
+    for i in range(0, T, 1000):
+        ea.attn_kv4_append(k[i:i + 1000], v[i:i + 1000], b, i32(slots[i:i + 1000]), signs=signs)
+    assert torch.equal(a, b) and a.any()
+    big = ea.attn_kv4_read(a, i32(slots), dtype=torch.float32)
+    for i in range(0, T, 5000):
+        small = ea.attn_kv4_read(a, i32(slots[i:i + 5000]), dtype=torch.float32)
+        assert all(torch.equal(x[i:i + 5000], y) for x, y in zip(big, small))
+    assert (big[0][::17] == 0).all() and ea.attn_device_status() == ea.ATTN_OK
+
+
 def test_slots_of_nobody_and_slots_out_of_range():
     Hk, d, page, nb = 2, 64, 16, 2
     k, v = _kv(5, 6, Hk, d)
