@@ -68,7 +68,7 @@ struct ChunkCfg {
   static constexpr int kSmem = kRawOff + kRawSlots * kRawBytes + 1024;  // room to align to 1024 bytes
   static constexpr int kOCol = 256;
   static constexpr int kTmemCols = 512;
-  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + 3072 <= 227 * 1024, "shared memory");
 };
 
 // What is known of a block of keys from its scales
@@ -79,7 +79,7 @@ struct alignas(16) BlockInfo {
   uint32_t special;  // not zero: some tile is not there, or some V is not finite
   uint32_t odd[4];   // one bit per key: its V is not finite (and is held as zero in shared memory)
 };
-// Of them: the block that is read for, three in the ring of tiles, and the one whose softmax runs
+// Entries in use at most: a block whose tiles have come, three before it in the ring, and one more whose softmax runs
 constexpr int kInfos = 8;
 
 struct ChunkWalk {
@@ -871,8 +871,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
           }
           exp_v = max(exp_v, e[1]);
           if (lane == 0) {
-            // read last for block blk - 8, whose tiles the ring has long let go of, and its softmax too: the K of block
-            // blk - 4 came after that block's V had been multiplied
+            // the entry's last block was blk - 8: for this block's tiles the ring has let go of blk - 3, whose V came after
+            // S of blk - 4, and that after the softmax of blk - 5
             BlockInfo& bi = info[blk % kInfos];
             bi.k_back = exp2_int(e[0]), bi.v_exp = exp_v, bi.gone = gone;
             bi.special = gone | odds[0] | odds[1] | odds[2] | odds[3];

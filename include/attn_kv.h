@@ -123,8 +123,8 @@ int attn_kv4_read(const void* cache, const int* slots, void* k, void* v, int T, 
 
 /*
  * attn_fwd_kv4_workspace_bytes -- bytes of the workspace attn_fwd_kv4 needs for these arguments, whatever the lengths of
- * the requests are: partial results (20 to 40 MB), and where a request may have more than 32 rows per key/value head (at
- * d = 64, 128) a float16 copy of Q.  num_sms 0: of the current device.  0 for arguments that attn_fwd_kv4 would refuse,
+ * the requests are: partial results (15 to 40 MB), and where a request may have more rows per key/value head than the
+ * few of attn_fwd_kv4 a float16 copy of Q.  num_sms 0: of the current device.  0 for arguments that attn_fwd_kv4 would refuse,
  * or where there is no device to ask.
  */
 unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total_q, int max_seqlen_q, int d, int num_sms);
@@ -145,8 +145,9 @@ unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total
  *   signs       as given to attn_kv4_append: Q is transformed alike.  NULL: none.
  *   causal      1: key j is visible to query i of a request iff j <= i + seq_len - query_len (the new
  *               tokens are the last ones); 0: every key.  A row with no key gets O = 0, LSE = -inf.
- *   workspace   attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, 0) bytes, 16-byte aligned, overwritten; not shared by calls
- *               that may run at the same time.
+ *   workspace   attn_fwd_kv4_workspace_bytes(B, Hq, Hk, total_q, max_seqlen_q, d, 0) bytes, 16-byte aligned,
+ *               overwritten; not shared by calls that may run at the same time.
+ * Neither o nor lse may overlap any other array.
  * Arithmetic: softmax and sums in float32.  Requests of few rows (queries times Hq / Hk; up to 64 at d = 64, 48 at
  * d = 128, any number at d = 256): the codes are multiplied as they are, Q in 22 bits (each row scaled by a power
  * of two), P times the step of V rounded to float16.  Others: Q (transformed), K, V and P rounded to float16 under
