@@ -162,3 +162,27 @@ def test_random_shapes(seed):
     ctx = [int(x) for x in rng.integers(0, int(rng.choice([20, 300, 1500])), B)]
     _run(ctx, nq, Hk * G, Hk, int(rng.choice([64, 128, 256])), int(rng.choice([16, 48, 64, 128])), bool(rng.integers(2)),
          bool(rng.integers(2)), seed)
+
+
+@pytest.mark.parametrize("d,Hq,Hk,B", [(64, 3, 1, 1100), (128, 4, 2, 900), (128, 9, 1, 500), (256, 2, 1, 700)])
+def test_more_requests_than_threads(d, Hq, Hk, B):
+    """Several requests per thread of the pass that cuts the work into spans, many of them without keys or queries."""
+    rng = np.random.default_rng(d)
+    ctx = [int(x) for x in rng.integers(0, 50, B) * rng.integers(0, 2, B)]
+    _run(ctx, rng.integers(0, 3, B), Hq, Hk, d, 16, True, d == 128, seed=d)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 12), (128, 4), (128, 12), (256, 3)])
+def test_one_request_over_every_span(d, G):
+    """A chunk of rows whose parts are more than the join looks over at once, with a short request on either side."""
+    _run([3, 90000, 40], [1, 1, 1], G, 1, d, 64, True, True, seed=d + G)
+
+
+@pytest.mark.parametrize("bound", [1, 200])
+def test_a_batch_without_queries(bound):
+    rng = np.random.default_rng(0)
+    table, nb = random_table(rng, [40, 20], 16)
+    cache = filled_cache(rng, [40, 20], table, nb, 1, 128, 16)
+    o, lse = torch.full((3, 2, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((2, 3), 5.0, device="cuda")
+    ea.attn_fwd_kv4(_q(rng, 3, 2, 128), cache, i32(table), i32([40, 20]), i32([0, 0, 0]), bound, o=o, lse=lse)
+    assert ea.attn_device_status() == ea.ATTN_OK and (o == 5).all() and (lse == 5).all()
