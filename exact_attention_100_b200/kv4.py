@@ -171,8 +171,14 @@ def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse,
     at = _arg(positions, (len(sections), N) if q.dim() == 3 else (len(sections), B, N), torch.int32, "positions", dev)
     out_dtype = out_dtype or (q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else q.dtype)
     if q_out is None:
+        if out_dtype not in types:
+            raise ValueError("the results are bf16 or float32")
         q_out = torch.empty_like(q, dtype=out_dtype)
-    strides, pqo = _rows(q_out, q.shape, types, "q_out", dev)
+        strides, pqo = q_out.stride(), q_out.data_ptr()
+        if strides[-1] != 1:
+            raise ValueError("q's rows must not overlap")
+    else:
+        strides, pqo = _rows(q_out, q.shape, types, "q_out", dev)
     strides_qo = _dims(q_out, strides)[1]
     strides_k = strides_ko = (8, 8, 8)
     Hk = pk = pko = 0
@@ -183,7 +189,11 @@ def _rope(q, k, cos, sin, positions, sections, q_out, k_out, out_dtype, inverse,
             raise ValueError("k must have q's tokens and d")
         if k_out is None:
             k_out = torch.empty_like(k, dtype=q_out.dtype)
-        strides, pko = _rows(k_out, k.shape, (q_out.dtype,), "k_out", dev)
+            strides, pko = k_out.stride(), k_out.data_ptr()
+            if strides[-1] != 1:
+                raise ValueError("k's rows must not overlap")
+        else:
+            strides, pko = _rows(k_out, k.shape, (q_out.dtype,), "k_out", dev)
         strides_ko = _dims(k_out, strides)[1]
     elif k_out is not None:
         raise ValueError("k_out without k")

@@ -127,3 +127,13 @@ def test_binding_refuses(bad):
         ea.attn_rope_axes(q, None, cos, sin, pos, bad.get("sections", [32]),
                           q_out=q.view(4, 2, 64)[:3] if "out" in bad else None)
     assert ea.attn_num_kernel_launches() == before
+
+
+def test_binding_refuses_other_types_and_rows_that_overlap():
+    cos, sin = _tables(10, 32)
+    q, pos = torch.zeros(4, 2, 64, device="cuda", dtype=BF), i32(np.zeros((1, 4)))
+    before = ea.attn_num_kernel_launches()
+    for bad in (dict(out_dtype=torch.float16), dict(q_out=q.half()), dict(k=q[:, :1].expand(4, 2, 64)), dict(q=q[:1].expand(4, 2, 64))):
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_rope_axes(bad.get("q", q), bad.get("k"), cos, sin, pos, [32], q_out=bad.get("q_out"), out_dtype=bad.get("out_dtype"))
+    assert ea.attn_num_kernel_launches() == before
