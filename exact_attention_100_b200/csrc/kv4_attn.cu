@@ -53,10 +53,11 @@ namespace {
 constexpr int kKeys = 32;
 // What a chunk costs besides its units (its Q, its O), in units
 constexpr int kChunkCost = 4;
-// Requests of more rows per key/value head than this go to the chunk kernel (d = 64, 128), whose tiles of 128 rows take
-// the same time from 1 row on.  8 requests of 8,192 keys, 8 heads, d = 128, this kernel and that one: 78 and 115 us
-// for 32 rows, 104 and 112 for 48, 134 and 113 for 64; d = 64: 66 and 96 for 48, 83 and 97 for 64, 118 and 96 for 96.
-constexpr int chunk_min_rows(int d) { return d == 64 ? 64 : 48; }
+// Requests of more rows per key/value head than this go to the chunk kernel, whose tiles of 128 rows take the same
+// time from 1 row on.  8 requests of 8,192 keys, 8 heads, d = 128, this kernel and that one: 78 and 115 us
+// for 32 rows, 104 and 112 for 48, 134 and 113 for 64; d = 64: 66 and 96 for 48, 83 and 97 for 64, 118 and 96 for 96;
+// d = 256: 106 and 140 for 24, 136 and 141 for 32, 165 and 140 for 40.
+constexpr int chunk_min_rows(int d) { return d == 64 ? 64 : d == 128 ? 48 : 32; }
 // Units after which the sums of codes are centred
 constexpr int kCentre = 16;
 
@@ -880,7 +881,7 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 // Whether some request may go to the chunk kernel.
-bool may_chunk(long long max_q, int G, int d) { return d <= 128 && max_q * G > chunk_min_rows(d); }
+bool may_chunk(long long max_q, int G, int d) { return max_q * G > chunk_min_rows(d); }
 
 unsigned long long kv4_attn_workspace_bytes(int B, int Hk, int G, long long total_q, int max_q, int d, int num_sms) {
   unsigned long long n = 0;

@@ -1,8 +1,9 @@
-// Attention of many query rows over the 4-bit paged cache: prompts taken in chunks (d = 64, 128).
+// Attention of many query rows over the 4-bit paged cache: prompts taken in chunks.
 //
 // The rows of a request that share a key/value head (its queries times Hq / Hk heads) are cut into chunks of
 // 256, two tiles of 128 rows; a chunk runs over the keys in blocks of 128 with tcgen05 products into tensor
 // memory, S = Q K^T and O += P V, the two tiles taking turns at the tensor core while the other's softmax runs.
+// At d = 256 O of one tile takes half of tensor memory: chunks of 128 rows, one tile, blocks of 64 keys.
 // Bound by arithmetic: 4 d flops per row and key for 1.125 d bytes per key, so the codes are brought to float16
 // in shared memory once per block and used by both tiles.
 //
@@ -46,8 +47,6 @@ namespace ea {
 
 namespace {
 
-constexpr int kRowsPerChunk = 256;
-constexpr int kBlockKeys = 128;
 // What a chunk costs besides its blocks (its Q, its O, no overlap at its ends), in blocks
 constexpr int kChunkCost = 3;
 // A span has at least this much work
@@ -56,14 +55,21 @@ constexpr int kMinCost = 2;
 template <int D>
 struct ChunkCfg {
   static constexpr int kThreads = 608;
-  static constexpr int kBoxes = D / 64;                 // 64-dimension halves, rows of 128 bytes
-  static constexpr int kBoxBytes = 128 * 128;
-  static constexpr int kTileBytes = kBoxes * kBoxBytes;  // 128 rows x D float16
+  // d = 256: O of one tile takes half of tensor memory, Q of one 64 KB, so one tile, and blocks of 64 keys
+  static constexpr int kRows = D == 256 ? 128 : 256;    // of a chunk
+  static constexpr int kKeys = D == 256 ? 64 : 128;     // of a block
+  static constexpr int kTiles = kRows / 128;
+  static constexpr int kPairs = kKeys / 32;             // of the cache's tiles in a block
+  static constexpr int kBoxes = D / 64;                 // 64-dimension pieces, rows of 128 bytes
+  static constexpr int kQBoxBytes = 128 * 128;
+  static constexpr int kQTileBytes = kBoxes * kQBoxBytes;  // 128 rows x D float16
+  static constexpr int kBoxBytes = kKeys * 128;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;    // kKeys keys x D float16
   static constexpr int kSlots = 3;                      // of K and V tiles, by turns
-  static constexpr int kRawSlots = 14;                  // pairs of the cache's tiles
+  static constexpr int kRawSlots = D == 256 ? 6 : 14;   // pairs of the cache's tiles
   static constexpr int kRawBytes = 2 * Kv4Tile<D>::kBytes;
   static constexpr int kQOff = 0;
-  static constexpr int kKvOff = 2 * kTileBytes;
+  static constexpr int kKvOff = kTiles * kQTileBytes;
   static constexpr int kRawOff = kKvOff + kSlots * kTileBytes;
   static constexpr int kSmem = kRawOff + kRawSlots * kRawBytes + 1024;  // room to align to 1024 bytes
   static constexpr int kOCol = 256;
@@ -90,37 +96,41 @@ struct ChunkWalk {
   Segment seg;
 };
 
+template <int D>
 __device__ __forceinline__ int chunk_blocks(const Kv4AttnParams& p, const SeqLen& s, int chunk) {
-  const int last = min(s.nq * p.G, (chunk + 1) * kRowsPerChunk) - 1;
+  const int last = min(s.nq * p.G, (chunk + 1) * ChunkCfg<D>::kRows) - 1;
   const int lim = p.causal ? min(s.nk, s.nk - s.nq + last / p.G + 1) : s.nk;
-  return max(1, (lim + kBlockKeys - 1) / kBlockKeys);
+  return lim > 0 ? static_cast<int>((static_cast<unsigned>(lim) + ChunkCfg<D>::kKeys - 1) / ChunkCfg<D>::kKeys) : 1;
 }
+template <int D>
 __device__ __forceinline__ int chunk_count(const Kv4AttnParams& p, const SeqLen& s) {
-  return static_cast<int>((static_cast<long long>(s.nq) * p.G + kRowsPerChunk - 1) / kRowsPerChunk);
+  return static_cast<int>((static_cast<long long>(s.nq) * p.G + ChunkCfg<D>::kRows - 1) / ChunkCfg<D>::kRows);
 }
+template <int D>
 __device__ __forceinline__ long long request_cost(const Kv4AttnParams& p, const SeqLen& s) {
-  const int n = chunk_count(p, s);
+  const int n = chunk_count<D>(p, s);
   long long sum = 0;
-  for (int i = 0; i < n; ++i) sum += chunk_blocks(p, s, i) + kChunkCost;
+  for (int i = 0; i < n; ++i) sum += chunk_blocks<D>(p, s, i) + kChunkCost;
   return sum * p.Hk;
 }
 
 // The next segment of a walk (one lane): false when the span has ended.  A boundary inside the cost in front
 // of a chunk counts as the chunk's start.
+template <int D>
 __device__ __noinline__ bool next_segment(const Kv4AttnParams& p, volatile ChunkWalk& w) {
   long long pos = w.pos, first = w.first;
   const long long end = w.end;
   int b = w.b, chunk = w.chunk, chunks = w.chunks;
   SeqLen s = seq_len(p, b);
-  if (chunks < 0) chunks = chunk_count(p, s);
+  if (chunks < 0) chunks = chunk_count<D>(p, s);
   bool found = false;
   while (pos < end && !found) {
     while (chunk >= chunks) {
       s = seq_len(p, ++b);
       chunk = 0;
-      chunks = chunk_count(p, s);
+      chunks = chunk_count<D>(p, s);
     }
-    const int blocks = chunk_blocks(p, s, chunk), each = blocks + kChunkCost;
+    const int blocks = chunk_blocks<D>(p, s, chunk), each = blocks + kChunkCost;
     const long long rel = pos - first;
     if (rel >= static_cast<long long>(each) * p.Hk) {
       first += static_cast<long long>(each) * p.Hk;
@@ -144,9 +154,10 @@ __device__ __noinline__ bool next_segment(const Kv4AttnParams& p, volatile Chunk
 }
 
 // One warp's look at the next segment.
+template <int D>
 __device__ __forceinline__ bool take_segment(const Kv4AttnParams& p, volatile ChunkWalk& w, int lane, Segment& seg) {
   __syncwarp();
-  if (lane == 0) w.more = next_segment(p, w) ? 1 : 0;
+  if (lane == 0) w.more = next_segment<D>(p, w) ? 1 : 0;
   __syncwarp();
   if (!w.more) return false;
   seg.b = w.seg.b, seg.h = w.seg.h, seg.chunk = w.seg.chunk;
@@ -216,19 +227,19 @@ __device__ __forceinline__ float exps(const uint32_t (&r)[32], uint32_t (&pk)[16
 // The reference moves when the p of 32 keys come to more than this (no one of them is more, then, if they do not)
 constexpr float kSumMost = 256.f;
 
-// Q of a chunk of rows as the products take it: two tiles of 128 rows x D float16 as they lie in shared memory, then
-// [256] factors of the rows' scores, written ahead by kv4_chunk_q_kernel.  Request b's chunks start at q0 G / 256 + b,
+// Q of a chunk of rows as the products take it: its tiles of 128 rows x D float16 as they lie in shared memory, then the
+// factors of the rows' scores, written ahead by kv4_chunk_q_kernel.  Request b's chunks start at q0 G / rows + b,
 // so those of different requests do not meet.
 template <int D>
-constexpr size_t q_image_bytes() { return kRowsPerChunk * (D * 2 + 4); }
+constexpr size_t q_image_bytes() { return ChunkCfg<D>::kRows * (D * 2 + 4); }
 template <int D>
 __device__ __forceinline__ uint8_t* q_image(const Kv4AttnParams& p, int b, int q0, int chunk, int h) {
-  const long long first = static_cast<long long>(q0) * p.G / kRowsPerChunk + b;
+  const long long first = static_cast<long long>(q0) * p.G / ChunkCfg<D>::kRows + b;
   return p.ws_q + ((first + chunk) * p.Hk + h) * q_image_bytes<D>();
 }
 template <int D>
 __device__ __forceinline__ const float* q_factor(const Kv4AttnParams& p, const Segment& s) {
-  return reinterpret_cast<const float*>(q_image<D>(p, s.b, s.q0, s.chunk, s.h) + kRowsPerChunk * D * 2);
+  return reinterpret_cast<const float*>(q_image<D>(p, s.b, s.q0, s.chunk, s.h) + ChunkCfg<D>::kRows * D * 2);
 }
 
 // One warp per row of a request (and key/value head): transformed in float32, scaled by a power of two that puts its
@@ -238,10 +249,11 @@ constexpr int kQWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4AttnParams p) {
   constexpr int E = D / 32;  // consecutive entries of a lane
+  constexpr int ROWS = ChunkCfg<D>::kRows;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.z, h = blockIdx.y;
   const SeqLen s = seq_len(p, b);
-  const int rows = s.nq * p.G, padded = (rows + kRowsPerChunk - 1) / kRowsPerChunk * kRowsPerChunk;
+  const int rows = s.nq * p.G, padded = (rows + ROWS - 1) / ROWS * ROWS;
   for (int row = blockIdx.x * kQWarps + (threadIdx.x >> 5); row < padded; row += gridDim.x * kQWarps) {
     const int tok = row / p.G, hq = h * p.G + row - tok * p.G;
     uint32_t w[E / 2];
@@ -249,7 +261,10 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
     for (int e = 0; e < E / 2; ++e) w[e] = 0u;
     if (row < rows) {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (s.q0 + tok) * p.q_sn + hq * p.q_sh + E * lane;
-      if constexpr (E == 4) {
+      if constexpr (E == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else if constexpr (E == 4) {
         const uint2 v = *reinterpret_cast<const uint2*>(src);
         w[0] = v.x, w[1] = v.y;
       } else {
@@ -289,12 +304,15 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     const int ex = bits != 0u ? min(max(exponent_of(__uint_as_float(bits)) - 13, -100), 100) : 0;
     const float f = exp2_int(-ex);
-    const int chunk = row / kRowsPerChunk, cr = row - chunk * kRowsPerChunk, tr = cr & 127;
+    const int chunk = row / ROWS, cr = row - chunk * ROWS, tr = cr & 127;
     uint8_t* image = q_image<D>(p, b, s.q0, chunk, h);
     // entries 0 .. 7 of a 16-byte piece lie in 8 / E lanes; each stores its share of the pairs (0, 4) (1, 5) (2, 6) (3, 7)
-    uint8_t* at = image + (cr >> 7) * ChunkCfg<D>::kTileBytes + (lane * E / 64) * ChunkCfg<D>::kBoxBytes + tr * 128 +
+    uint8_t* at = image + (cr >> 7) * ChunkCfg<D>::kQTileBytes + (lane * E / 64) * ChunkCfg<D>::kQBoxBytes + tr * 128 +
                   ((((lane * E / 8) & 7) ^ (tr & 7)) << 4);
-    if constexpr (E == 4) {
+    if constexpr (E == 8) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(pack_f16x2(x[0] * f, x[4] * f), pack_f16x2(x[1] * f, x[5] * f),
+                                                 pack_f16x2(x[2] * f, x[6] * f), pack_f16x2(x[3] * f, x[7] * f));
+    } else if constexpr (E == 4) {
       const bool up = lane & 1;  // entries 4 .. 7
       const float s0 = __shfl_xor_sync(0xffffffffu, up ? x[0] : x[2], 1);
       const float s1 = __shfl_xor_sync(0xffffffffu, up ? x[1] : x[3], 1);
@@ -307,7 +325,7 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
           up ? pack_f16x2(s0 * f, x[1] * f) : pack_f16x2(x[0] * f, s0 * f);
     }
     if (lane == 0)
-      reinterpret_cast<float*>(image + kRowsPerChunk * D * 2)[cr] = p.scale_log2 * exp2_int(ex);
+      reinterpret_cast<float*>(image + ROWS * D * 2)[cr] = p.scale_log2 * exp2_int(ex);
   }
 }
 
@@ -322,7 +340,7 @@ template <int D>
 __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(const Kv4AttnParams p) {
   using C = ChunkCfg<D>;
   using F = Kv4Tile<D>;
-  constexpr int ROWS = kRowsPerChunk;
+  constexpr int ROWS = C::kRows, KEYS = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots];
@@ -366,7 +384,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   for (int b = my0; b < my1; ++b) {
     const SeqLen s = seq_len(p, b);
     bad |= s.bad;
-    mine += request_cost(p, s);
+    mine += request_cost<D>(p, s);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.status, kDevStatusBadSeqlens);
   long long before = mine;
@@ -396,7 +414,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   if (before <= span0 && span0 < before + mine) {  // one thread: the span starts in its run
     int b = my0;
     for (;; ++b) {
-      const long long n = request_cost(p, seq_len(p, b));
+      const long long n = request_cost<D>(p, seq_len(p, b));
       if (span0 < before + n) break;
       before += n;
     }
@@ -433,7 +451,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
     Meta found{};
     bool ok = true;
     Segment S;
-    while (ok && take_segment(p, walks[warp], lane, S)) {
+    while (ok && take_segment<D>(p, walks[warp], lane, S)) {
       const int row0 = S.chunk * ROWS, rows = min(ROWS, S.nq * p.G - row0);
       const bool starts = S.t0 == 0, ends = S.t1 == S.units;
       if (starts && !ends) {
@@ -466,8 +484,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         const uint4 known = *reinterpret_cast<const uint4*>(&bi);
         const float c = c_row * __uint_as_float(known.x);
         const int ve = static_cast<int>(known.y);
-        const int lim = lim_row - t * kBlockKeys;
-        const bool need_mask = (t + 1) * kBlockKeys > lim_first || known.w != 0;
+        const int lim = lim_row - t * KEYS;
+        const bool need_mask = (t + 1) * KEYS > lim_first || known.w != 0;
         float alpha = 1.f;
         float l_blk = 0.f;  // of p under the reference at hand
         // 32 keys at a time, p under the reference at hand; only where they come to too much the reference moves,
@@ -478,7 +496,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         if (!need_mask) {
           bool over = false;
 #pragma unroll 1
-          for (int k2 = 0; k2 < 4 && !over; k2 += 2) {
+          for (int k2 = 0; k2 < KEYS / 32 && !over; k2 += 2) {
             uint32_t a[32], b[32], pk[16];
             tmem_ld_32cols(tS + 32 * k2, a);
             tmem_ld_32cols(tS + 32 * k2 + 32, b);
@@ -498,9 +516,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
             k0 = k2 + 2;
           }
         }
-        const bool moved = k0 < 4;
+        const bool moved = k0 < KEYS / 32;
 #pragma unroll 1
-        for (int k = k0; k < 4; ++k) {
+        for (int k = k0; k < KEYS / 32; ++k) {
           uint32_t r[32], pk[16];
           tmem_ld_32cols(tS + 32 * k, r);
           tmem_ld_wait(r);
@@ -617,18 +635,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   } else if (warp < 16) {
     // ================================================================ codes to float16: K of a block, then its V
     const int ct = tid - 256;
-    const int c = ct & 3, r = (ct >> 2) & 15, ti = (ct >> 6) & 1;  // keys 64 i + ct / 4, i = 0, 1
+    // keys 64 i + ct / 4, i = 0, 1, or at d = 256 key ct / 4, planes of 128 dimensions i = 0, 1
+    const int c = ct & 3, r = (ct >> 2) & 15, ti = (ct >> 6) & 1;
+    constexpr bool kPlanes = F::kPlanes == 2;
     // where this thread's 16-byte pieces of its key 0 go; the second one of 8 dimensions is at ^ 16
     const int put_at = (ct >> 2) * 128 + (((2 * c) ^ ((ct >> 2) & 7)) << 4);
     uint32_t blk = 0, pair = 0;
     bool ok = true;
     Segment S;
-    while (ok && take_segment(p, walks[warp], lane, S)) {
-      for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += 4) {
-        // the block's scales have been looked at, and this warp's two pairs of tiles are there (as they are then)
+    while (ok && take_segment<D>(p, walks[warp], lane, S)) {
+      for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += C::kPairs) {
+        // the block's scales have been looked at, and this warp's pairs of tiles are there (as they are then)
         ok = wait_bar(&info_full[blk % kInfos], (blk / kInfos) & 1u, ab);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < (kPlanes ? 1 : 2); ++i) {
           const uint32_t mine = pair + 2 * i + (ct >> 7);
           ok = ok && wait_bar(&raw_full[mine % C::kRawSlots], (mine / C::kRawSlots) & 1u, ab);
         }
@@ -640,19 +660,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         for (int v = 0; v < 2 && ok; ++v) {
           const uint32_t item = 2 * blk + v, slot = item % C::kSlots;
           const float f = exp2_int(-(v ? static_cast<int>(known.y) : exponent_of(__uint_as_float(known.x))));
-          const int codes_at = ti * F::kBytes + v * F::kVOff + r * F::kRowBytes + 8 * (D / 64) * c;
+          const int codes_at = ti * F::kBytes + v * F::kVOff + r * F::kRowBytes + 8 * F::kGroups * c;
           const int sz_at = ti * F::kBytes + (v ? F::kVszOff : F::kKszOff) + r * F::kSzRow;
           ok = warp_all(wait_bar(&kv_empty[slot], ((item / C::kSlots) & 1u) ^ 1u, ab));
           if (!ok) break;
           uint8_t* to = smem + C::kKvOff + slot * C::kTileBytes;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int key = 64 * i + (ct >> 2);
-            const uint8_t* raw = smem + C::kRawOff + ((pair + 2 * i + (ct >> 7)) % C::kRawSlots) * C::kRawBytes;
-            uint32_t w[2 * (D / 64)], sz[D / 64];  // [8 dimensions][group]
-            if constexpr (D == 128) {
-              const uint4 a = *reinterpret_cast<const uint4*>(raw + codes_at);
-              const uint2 b = *reinterpret_cast<const uint2*>(raw + sz_at);
+            const int key = (kPlanes ? 0 : 64 * i) + (ct >> 2);
+            const uint8_t* raw = smem + C::kRawOff + ((pair + (kPlanes ? 0 : 2 * i) + (ct >> 7)) % C::kRawSlots) * C::kRawBytes;
+            uint32_t w[2 * F::kGroups], sz[F::kGroups];  // [8 dimensions][group]
+            const int plane = kPlanes ? i : 0;
+            if constexpr (F::kGroups == 2) {
+              const uint4 a = *reinterpret_cast<const uint4*>(raw + codes_at + plane * F::kPlaneBytes);
+              const uint2 b = *reinterpret_cast<const uint2*>(raw + sz_at + 8 * plane);
               w[0] = a.x, w[1] = v ? a.y : a.z, w[2] = v ? a.z : a.y, w[3] = a.w;
               sz[0] = b.x, sz[1] = b.y;
             } else {
@@ -662,28 +683,28 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
             }
             // absent keys are zero; so is a V that is not finite (the rows that see it become NaN by its bit of odd;
             // the others must not see it)
-            bool zero = t * kBlockKeys + key >= S.nk;
+            bool zero = t * KEYS + key >= S.nk;
             if (known.w != 0) zero = zero || ((known.z >> (key >> 4)) & 1u) || (v && ((bi.odd[key >> 5] >> (key & 31)) & 1u));
 #pragma unroll
-            for (int g = 0; g < D / 64; ++g) {
+            for (int g = 0; g < F::kGroups; ++g) {
               const Scales sc = scales_of(zero ? 0u : sz[g], f);
-              uint8_t* at = to + g * C::kBoxBytes + i * (64 * 128);
+              uint8_t* at = to + (F::kGroups * plane + g) * C::kBoxBytes + (kPlanes ? 0 : i * (64 * 128));
               *reinterpret_cast<uint4*>(at + put_at) = expand(w[g], sc);
-              *reinterpret_cast<uint4*>(at + (put_at ^ 16)) = expand(w[(D / 64) + g], sc);
+              *reinterpret_cast<uint4*>(at + (put_at ^ 16)) = expand(w[F::kGroups + g], sc);
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&kv_full[slot]);
         }
-        if (lane < 4) bar_arrive(&raw_empty[(pair + lane) % C::kRawSlots]);
+        if (lane < C::kPairs) bar_arrive(&raw_empty[(pair + lane) % C::kRawSlots]);
         __syncwarp();
       }
     }
   } else {
     if (warp == 16) {
       // ============================================================== MMA issuer
-      constexpr uint32_t kIdS = make_idesc(128, 128, 0, false);  // float16, both K-major
+      constexpr uint32_t kIdS = make_idesc(128, KEYS, 0, false);  // float16, both K-major
       constexpr uint32_t kIdPV = make_idesc(128, D, 0, true);    // V MN-major
       constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row atoms, version, 128-byte swizzle
       const uint32_t base_u = __shfl_sync(0xffffffffu, smem_addr(smem), 0), tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
@@ -696,12 +717,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       };
       uint32_t blk = 0, n_p = 0, n_q = 0;  // n_p, n_q: bit q is the parity of tile q's next phase
       auto issue_s = [&](int q, uint32_t item) {
-        const uint32_t d = tmem_u + q * 128, a = q_lo + q * (C::kTileBytes >> 4);
+        const uint32_t d = tmem_u + q * 128, a = q_lo + q * (C::kQTileBytes >> 4);
         const uint32_t b = (kv_lo + item * (C::kTileBytes >> 4)) | (1u << 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4;
-          mma_f16_ss(d, desc(a + off), desc(b + off), kIdS, kk > 0 ? 1u : 0u);
+          const uint32_t qo = ((kk / 4) * C::kQBoxBytes + (kk % 4) * 32) >> 4, ko = ((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4;
+          mma_f16_ss(d, desc(a + qo), desc(b + ko), kIdS, kk > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[q]);
       };
@@ -709,12 +730,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         const uint32_t d = tmem_u + C::kOCol + q * D, a = tmem_u + q * 128;
         const uint32_t b = (kv_lo + item * (C::kTileBytes >> 4)) | (static_cast<uint32_t>(C::kBoxBytes >> 4) << 16);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = 0; kk < KEYS / 16; ++kk)
           mma_f16_ts(d, a + kk * 8, desc(b + kk * (16 * 128 >> 4)), kIdPV, (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
       Segment S;
-      while (ok && take_segment(p, walks[warp], lane, S)) {
+      while (ok && take_segment<D>(p, walks[warp], lane, S)) {
         const int tiles = min(ROWS, S.nq * p.G - S.chunk * ROWS) > 128 ? 2 : 1;
         {
           const int n = S.t1 - S.t0;
@@ -767,20 +788,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       uint32_t pair = 0, n_q[2] = {0, 0};
       bool ok = true;
       Segment S;
-      while (ok && take_segment(p, walks[warp], lane, S)) {
+      while (ok && take_segment<D>(p, walks[warp], lane, S)) {
         // Q's tiles, once the products of the segment before have read theirs
         const uint8_t* image = q_image<D>(p, S.b, S.q0, S.chunk, S.h);
         const int tiles = min(ROWS, S.nq * p.G - S.chunk * ROWS) > 128 ? 2 : 1;
         auto load_q = [&]() {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < C::kTiles; ++q) {
             if (q >= tiles || !ok) break;
             ok = warp_all(wait_bar(&q_empty[q], (n_q[q] & 1u) ^ 1u, ab));
             if (!ok) break;
             ++n_q[q];
             if (lane == 0) {
-              bar_arrive_expect_tx(&q_full[q], C::kTileBytes);
-              bulk_load_g2s(smem + C::kQOff + q * C::kTileBytes, image + q * C::kTileBytes, C::kTileBytes, &q_full[q]);
+              bar_arrive_expect_tx(&q_full[q], C::kQTileBytes);
+              bulk_load_g2s(smem + C::kQOff + q * C::kQTileBytes, image + q * C::kQTileBytes, C::kQTileBytes, &q_full[q]);
             }
             __syncwarp();
           }
@@ -788,9 +809,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
         const uint8_t* next = nullptr;
         int state = 0;  // of this lane's tile of the block: 0 past the keys, 1 there, 2 no block of the cache
         auto look = [&](int t) {
-          const int key = t * kBlockKeys + 16 * lane;
+          const int key = t * KEYS + 16 * lane;
           state = 0;
-          if (lane < 8 && t < S.t1 && key < S.nk) {
+          if (lane < KEYS / 16 && t < S.t1 && key < S.nk) {
             const int j = key / p.page;
             const int e = __ldg(p.table + static_cast<long long>(S.b) * p.width + j);
             state = e >= 0 && e < p.num_blocks ? 1 : 2;
@@ -806,7 +827,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
           const uint32_t there = __ballot_sync(0xffffffffu, state == 1), gone = __ballot_sync(0xffffffffu, state == 2);
           look(t + 1);  // one block ahead of its copies
 #pragma unroll 1
-          for (int i = 0; i < 4 && ok; ++i, ++pair) {
+          for (int i = 0; i < C::kPairs && ok; ++i, ++pair) {
             const uint32_t slot = pair % C::kRawSlots;
             ok = warp_all(wait_bar(&raw_empty[slot], ((pair / C::kRawSlots) & 1u) ^ 1u, ab));
             if (!ok) break;
@@ -835,20 +856,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
       uint32_t blk = 0, pair = 0;
       bool ok = true;
       Segment S;
-      while (ok && take_segment(p, walks[warp], lane, S)) {
+      while (ok && take_segment<D>(p, walks[warp], lane, S)) {
         int exp_v = -100;  // of V: the largest so far
-        for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += 4) {
-          // the largest values, 4 keys per lane; a key that is not there, or not finite, counts as zero
+        for (int t = S.t0; t < S.t1 && ok; ++t, ++blk, pair += C::kPairs) {
+          // the largest values, a key of each pair per lane; a key that is not there, or not finite, counts as zero
           float top[2] = {0.f, 0.f};
-          uint32_t gone = 0, odds[4];
+          uint32_t gone = 0, odds[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < C::kPairs; ++i) {
             const uint32_t slot = (pair + i) % C::kRawSlots;
             ok = ok && warp_all(wait_bar(&raw_full[slot], ((pair + i) / C::kRawSlots) & 1u, ab));
             const uint32_t missing = raw_gone[slot];
             gone |= missing << (2 * i);
             const uint8_t* tile = smem + C::kRawOff + slot * C::kRawBytes + (lane >> 4) * F::kBytes + (lane & 15) * F::kSzRow;
-            const bool there = ok && !((missing >> (lane >> 4)) & 1u) && t * kBlockKeys + 32 * i + lane < S.nk;
+            const bool there = ok && !((missing >> (lane >> 4)) & 1u) && t * KEYS + 32 * i + lane < S.nk;
             bool odd = false;
 #pragma unroll
             for (int v = 0; v < 2; ++v)
@@ -895,11 +916,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1) kv4_chunk_kernel(con
   }
 }
 
+// The workspace: the spans' parts, then the images of Q.
+template <int D>
+unsigned long long image_offset(int num_sms) { return (part_bytes<D, ChunkCfg<D>::kRows>(num_sms) + 255) / 256 * 256; }
+template <int D>
+unsigned long long ws_bytes(int B, int Hk, int G, long long total_q, int num_sms) {
+  // a request's chunks start anew: at most one more than its rows fill
+  const unsigned long long chunks = static_cast<unsigned long long>(total_q * G / ChunkCfg<D>::kRows + B + 1) * Hk;
+  return image_offset<D>(num_sms) + chunks * q_image_bytes<D>();
+}
+
+template <int D>
+cudaError_t setup() {
+  return cudaFuncSetAttribute(kv4_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D>::kSmem);
+}
+
 template <int D>
 cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   using C = ChunkCfg<D>;
   Kv4AttnParams q = p;
-  q.ws_q = p.ws + (part_bytes<D, kRowsPerChunk>(num_sms) + 255) / 256 * 256;
+  q.ws_q = p.ws + image_offset<D>(num_sms);
   // a few rows per warp; requests shorter than the longest leave blocks without work
   const long long rows = static_cast<long long>(p.max_q) * p.G;
   const int per = static_cast<int>((rows + 4 * kQWarps - 1) / (4 * kQWarps));
@@ -909,27 +945,28 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
   kv4_chunk_kernel<D><<<num_sms, C::kThreads, C::kSmem, stream>>>(q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, kRowsPerChunk, 1>(q, num_sms, stream);
+  return launch_join<D, ChunkCfg<D>::kRows, 1>(q, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t setup_kv4_chunk_kernels() {
-  cudaError_t e = cudaFuncSetAttribute(kv4_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<64>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kv4_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<128>::kSmem);
+  cudaError_t e = setup<64>();
+  if (e == cudaSuccess) e = setup<128>();
+  if (e == cudaSuccess) e = setup<256>();
   return e;
 }
 
 unsigned long long kv4_chunk_workspace_bytes(int B, int Hk, int G, long long total_q, int d, int num_sms) {
-  // a request's chunks start anew: at most one more than its rows fill
-  const unsigned long long chunks = static_cast<unsigned long long>(total_q * G / kRowsPerChunk + B + 1) * Hk;
-  if (d == 64) return (part_bytes<64, kRowsPerChunk>(num_sms) + 255) / 256 * 256 + chunks * q_image_bytes<64>();
-  return (part_bytes<128, kRowsPerChunk>(num_sms) + 255) / 256 * 256 + chunks * q_image_bytes<128>();
+  if (d == 64) return ws_bytes<64>(B, Hk, G, total_q, num_sms);
+  if (d == 128) return ws_bytes<128>(B, Hk, G, total_q, num_sms);
+  return ws_bytes<256>(B, Hk, G, total_q, num_sms);
 }
 
 cudaError_t launch_kv4_chunk(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream) {
-  return d == 64 ? launch<64>(p, num_sms, stream) : launch<128>(p, num_sms, stream);
+  if (d == 64) return launch<64>(p, num_sms, stream);
+  if (d == 128) return launch<128>(p, num_sms, stream);
+  return launch<256>(p, num_sms, stream);
 }
 
 }  // namespace ea

@@ -68,7 +68,7 @@ def reference(q, ks, vs, cu, ctx, scale, causal, signs=None):
 
 # Requests with more rows (queries times heads per key/value head) than this go to the kernel that brings K and V to
 # float16
-FEW_ROWS = {64: 64, 128: 48, 256: 2 ** 31}
+FEW_ROWS = {64: 64, 128: 48, 256: 32}
 
 
 def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):

@@ -1,4 +1,4 @@
-"""attn_fwd_kv4 on requests of many rows (the tensor-memory kernel at d = 64, 128) and on batches that mix them with
+"""attn_fwd_kv4 on requests of many rows (the tensor-memory kernel) and on batches that mix them with
 requests of few rows; bounds as derived in kv_util.bounds."""
 
 import numpy as np
@@ -19,7 +19,7 @@ def _lib():
     ea_build.build()
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("transform", [False, True])
 @pytest.mark.parametrize("ctx,nq,Hq,Hk,page", [
     ([40], [40], 1, 1, 16), ([128], [128], 2, 2, 16), ([300], [100], 4, 1, 48), ([129, 640], [33, 129], 3, 3, 64),
@@ -28,24 +28,24 @@ def test_matches_the_oracle(d, transform, ctx, nq, Hq, Hk, page):
     _run(ctx, nq, Hq, Hk, d, page, True, transform, seed=sum(ctx) + d)
 
 
-@pytest.mark.parametrize("d,rows", [(64, 64), (64, 66), (128, 48), (128, 50)])
+@pytest.mark.parametrize("d,rows", [(64, 64), (64, 66), (128, 48), (128, 50), (256, 32), (256, 34)])
 def test_requests_on_both_sides_of_the_choice_of_kernel(d, rows):
     _run([rows, 210, 77], [rows // 2, rows // 2, 1], 4, 2, d, 16, True, True, seed=rows)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_without_the_causal_mask(d):
     _run([333, 1], [150, 40], 4, 2, d, 16, causal=False, transform=True, seed=d)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_rows_that_see_no_key(d):
     _, _, _, _, _, o, lse = _run([0, 30, 200], [50, 170, 60], 4, 2, d, 16, seed=d)
     assert (o[:50] == 0).all() and torch.isneginf(lse[:, :50]).all()
     assert (o[50:190] == 0).all() and (o[190] != 0).any()
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("q_std,k_std,v_std,scale", [(1e-3, 1e3, 1e-6, None), (30.0, 1.0, 1e5, None), (1.0, 1.0, 1e-25, None),
                                                      (1e-20, 1e20, 1.0, None), (4.0, 4.0, 1.0, 1.0)])
 def test_values_of_any_size(d, q_std, k_std, v_std, scale):
