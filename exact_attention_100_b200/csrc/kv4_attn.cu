@@ -51,8 +51,9 @@ namespace {
 // Keys of a unit: two tiles, which share one wait, one vote and one round of copies (a tile at a time
 // took 421 instructions per tile, a quarter of them for those)
 constexpr int kKeys = 32;
-// What a chunk costs besides its units (its Q, its O), in units
-constexpr int kChunkCost = 4;
+// What a chunk costs besides its units (its Q, its O), in units (the batch of the header and 8 requests of 2 to 5 tokens
+// at d = 256: 119 and 34.7 us with 3, 115 and 32.3 with 5, 117 and 32.9 with 8)
+constexpr int kChunkCost = 5;
 // Requests of more rows per key/value head than this go to the chunk kernel, whose tiles of 128 rows take the same
 // time from 1 row on.  8 requests of 8,192 keys, 8 heads, d = 128, this kernel and that one: 78 and 115 us
 // for 32 rows, 104 and 112 for 48, 134 and 113 for 64; d = 64: 66 and 96 for 48, 83 and 97 for 64, 118 and 96 for 96;

@@ -186,3 +186,9 @@ def test_a_batch_without_queries(bound):
     o, lse = torch.full((3, 2, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((2, 3), 5.0, device="cuda")
     ea.attn_fwd_kv4(_q(rng, 3, 2, 128), cache, i32(table), i32([40, 20]), i32([0, 0, 0]), bound, o=o, lse=lse)
     assert ea.attn_device_status() == ea.ATTN_OK and (o == 5).all() and (lse == 5).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq", [[1, 2, 1], [100, 1, 70]])
+def test_blocks_of_many_tokens(d, nq):
+    _run([5000, 3, 4097], nq, 4, 2, d, 4096, True, True, seed=d)
