@@ -76,7 +76,7 @@ def _device(torch, t):
     """The current CUDA device; a host tensor is refused before CUDA is asked for it."""
     if not t.is_cuda:
         raise ValueError(f"a {tuple(t.shape)} tensor is on {t.device}, not on the current CUDA device")
-    return torch._C._cuda_getDevice()
+    return torch._C._cuda_getDevice()  # CUDA is up, the tensor is on it
 
 
 def _again(f, stream, *args):
@@ -87,6 +87,7 @@ def _again(f, stream, *args):
 
 
 def _raw_stream(torch, dev):
+    # the handle alone: torch.cuda.current_stream() makes an object around it, 3 us
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -244,7 +245,7 @@ def _cache_dims(cache, torch, dev):
     if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be contiguous uint8 [num_blocks, Hk, page / 16, 18 d]")
     nb, hk, tiles, tile = shape
-    if cache.dtype is not torch.uint8 or not cache.is_contiguous():
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or not hk:
         raise ValueError("cache must be contiguous uint8 [num_blocks, Hk, page / 16, 18 d]")
     if cache.get_device() != dev:
         _refuse_device(cache, "cache")
@@ -265,6 +266,8 @@ def attn_kv4_append(k, v, cache, slots, signs=None, stream=None):
     import torch
     dev, bf16 = _device(torch, k), (torch.bfloat16,)
     nb, Hk, page, d, pc = _cache_dims(cache, torch, dev)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, Hk, d]")
     T = k.shape[0]
     ((kn, kh, _), pk), ((vn, vh, _), pv) = _rows(k, (T, Hk, d), bf16, "k", dev), _rows(v, (T, Hk, d), bf16, "v", dev)
     ps, pg = _arg(slots, (T,), torch.int32, "slots", dev), _sign_arg(signs, d, torch, dev)

@@ -192,3 +192,22 @@ def test_a_batch_without_queries(bound):
 @pytest.mark.parametrize("nq", [[1, 2, 1], [100, 1, 70]])
 def test_blocks_of_many_tokens(d, nq):
     _run([5000, 3, 4097], nq, 4, 2, d, 4096, True, True, seed=d)
+
+
+def test_binding_refuses_shapes_of_no_sense():
+    q, table, lens = torch.zeros(1, 2, 64, device="cuda", dtype=torch.bfloat16), i32([[0]]), i32([1])
+    good = ea.attn_kv4_cache(1, 1, 16, 64)
+    before = ea.attn_num_kernel_launches()
+    for cache in (good[:, :0], good[:0], good[..., :17], good[0], good.float(), good.cpu()):
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_fwd_kv4(q, cache, table, lens)
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_kv4_append(q[:, :1], q[:, :1], cache, i32([0]))
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_kv4_read(cache, i32([0]))
+    for bad in (q[0], q[0, 0, 0], q[:, :0], q.float(), q[..., :32], q[..., ::2]):
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_fwd_kv4(bad, good, table, lens)
+        with pytest.raises((ValueError, ea.AttnError)):
+            ea.attn_kv4_append(bad, bad, good, i32([0]))
+    assert ea.attn_num_kernel_launches() == before
