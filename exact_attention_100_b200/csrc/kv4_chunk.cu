@@ -29,7 +29,7 @@
 // Every operand is float16 (11 bits): Q, each row scaled by a power of two; K and V, u s + z in one fused
 // multiply-add, scaled by a power of two that puts the block's largest value (K) or the largest so far (V, O moves
 // with it as with the running maximum) at 2^-8 .. 2^-7; P, at most 2^8.  A score is off by two roundings of 2^-11 per
-// product (LSE by 5e-6 of itself at unit inputs); with bf16 operands it would be eight times that.  At that size the
+// product (LSE by 5e-7 of itself at unit inputs, see kv4_chunk_q_kernel); with bf16 operands it would be eight times that.  At that size the
 // step times 2^24 is a float16, and a nibble masked in place (the subnormal u 2^-24, or 16 u 2^-24) goes straight into
 // the multiply-add; values under a 64th of the largest keep fewer bits, 2^-18 of the largest.
 //
@@ -304,6 +304,23 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     const int ex = bits != 0u ? min(max(exponent_of(__uint_as_float(bits)) - 13, -100), 100) : 0;
     const float f = exp2_int(-ex);
+    // What the rounding leaves is split into its part along q, which the row's factor takes back (|q|^2 over q times the
+    // rounded q), and the rest.  Keys that weigh in lean towards q, so it was the part along q that moved LSE: off by
+    // 3.6e-6 of itself without this at 10,240 normal keys.
+    float along[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float a = x[e] * f;
+      along[0] = fmaf(a, a, along[0]);
+      along[1] = fmaf(a, __half2float(__float2half_rn(a)), along[1]);
+    }
+#pragma unroll
+    for (int st = 1; st < 32; st <<= 1) {
+      along[0] += __shfl_xor_sync(0xffffffffu, along[0], st);
+      along[1] += __shfl_xor_sync(0xffffffffu, along[1], st);
+    }
+    const float ratio = along[0] / along[1];
+    const float keep = fabsf(ratio - 1.f) < 0.01f ? ratio : 1.f;  // not for rows of zeros, infinities or NaN
     const int chunk = row / ROWS, cr = row - chunk * ROWS, tr = cr & 127;
     uint8_t* image = q_image<D>(p, b, s.q0, chunk, h);
     // entries 0 .. 7 of a 16-byte piece lie in 8 / E lanes; each stores its share of the pairs (0, 4) (1, 5) (2, 6) (3, 7)
@@ -325,7 +342,7 @@ __global__ void __launch_bounds__(kQWarps * 32) kv4_chunk_q_kernel(const Kv4Attn
           up ? pack_f16x2(s0 * f, x[1] * f) : pack_f16x2(x[0] * f, s0 * f);
     }
     if (lane == 0)
-      reinterpret_cast<float*>(image + ROWS * D * 2)[cr] = p.scale_log2 * exp2_int(ex);
+      reinterpret_cast<float*>(image + ROWS * D * 2)[cr] = p.scale_log2 * exp2_int(ex) * keep;
   }
 }
 
