@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     // largest entry at 2^13 .. 2^14 (back takes it back, and the 2^-24 of the codes).
     // A byte of codes is b = even + 16 odd, so with cb = q_odd / 16 and cn = q_even - cb the products
     // cn even + cb b are q_even even + q_odd odd.  Both are kept as two float16, the rounded value and what its
-    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).
+    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).  With the rounded values
+    // alone the batch of the header takes 103 us, but LSE is off by 3e-6 of itself instead of 3e-7.
     if (seg_no > 0) {
       mates = 1u << warp;
       set = 0, set_step = 1;
