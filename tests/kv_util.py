@@ -83,7 +83,8 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     V's step is rounded by 2^-11, which moves O by 2^-11 sum_j p_j (|v_j| + 15 s_j) <= 2^-11 3 sum_j p_j max|v_j| (a code
     times its step is at most the range, twice the largest value).
     Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18, x as above, and the row's
-    factor is corrected by sum q_i dq_i / sum q_i^2 <= 2^-11: 2^-11 |s_j| more; V is rounded by 2^-11, p too, twice where the maximum moved: 3 2^-11 sum_j p_j |v_j|.
+    factor is corrected by sum q_i dq_i / sum q_i^2 <= 2^-11: 2^-11 |s_j| more; V is rounded by 2^-11, p too, twice
+    where the maximum moved: 3 2^-11 sum_j p_j |v_j|.
     O is rounded to bf16, 2^-8.  Second order: the whole times 1.1."""
     q = q.float().cpu().numpy().astype(np.float64)
     if signs is not None:
