@@ -8,13 +8,12 @@
 // products: once per (key, row, group) instead of once per element.
 //
 // Long contexts are bound by memory (1.125 d bytes per key and key/value head) and, close behind, by the instructions
-// that this takes, about 540 per 32 keys at d = 128, 8 rows.  Rows of q are few, so the products are the warp's
-// m16n8 ones with keys (then dimensions) on the 16 side and rows on the 8 side, and the codes are operands as they
-// stand.  For K a word gives its even and its odd codes as bytes, 3 logic operations per 8 codes, and q is whole
-// numbers of two bytes: exact sums (m16n8k32).  For V p s is float16, and so must the codes be (m16n8k16): a byte
-// b = even + 16 odd of a word, and the even code alone, are float16 subnormals times 2^-24, which the tensor core
-// multiplies exactly, 4 logic operations per 8 codes and no conversion; even and odd dimensions are told apart at the
-// end.  Pairs of V run over two tokens: two byte permutes bring their words together.
+// that this takes: 560 per 32 keys at d = 128, 8 rows.  Rows of q are few, so the products are the warp's
+// m16n8k16 with keys (then dimensions) on the 16 side and rows on the 8 side: an operand register is then a pair of
+// bytes of a word of codes.  A byte b = even + 16 odd, and the even code alone, are float16 subnormals times 2^-24
+// as they stand, which the tensor core multiplies exactly: no conversion, 4 logic operations per 8 codes.  The
+// products of the pair give even and odd codes' shares after a change of basis of q (for K) or of O (for V).  Pairs of
+// V run over two tokens: two byte permutes bring their words together.
 //
 // One warp works on two tiles of 16 keys at a time and keeps its own running maximum, sum and O.  They
 // come through its own ring of shared-memory stages, filled by one bulk copy per tile (a tile with all its
@@ -37,7 +36,7 @@
 // join starts, 4.5 for it.  Each dependent read of what another processor wrote takes 0.6 us; the instructions
 // come from L2 the first time too (a quarter of the stalls).
 //
-// Measured: a batch of 48 with 1 to 16,384 keys, 32 heads over 8 of d = 128: 107 us, 4.2 TB/s (453 MB; 69 us at the
+// Measured: a batch of 48 with 1 to 16,384 keys, 32 heads over 8 of d = 128: 115 us, 3.9 TB/s (453 MB; 69 us at the
 // rate of a copy).
 
 #include <algorithm>
@@ -53,7 +52,7 @@ namespace {
 // took 421 instructions per tile, a quarter of them for those)
 constexpr int kKeys = 32;
 // What a chunk costs besides its units (its Q, its O), in units (the batch of the header and 8 requests of 2 to 5 tokens
-// at d = 256: 4 and 2 us more with 3, 2 and 0.6 more with 8)
+// at d = 256: 119 and 34.7 us with 3, 115 and 32.3 with 5, 117 and 32.9 with 8)
 constexpr int kChunkCost = 5;
 // Requests of more rows per key/value head than this go to the chunk kernel, whose tiles of 128 rows take the same
 // time from 1 row on.  8 requests of 8,192 keys, 8 heads, d = 128, this kernel and that one: 78 and 115 us
@@ -73,13 +72,13 @@ struct SplitCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlocksPerSm = D * NT <= 64 ? 2 : 1;
   static constexpr int kTile = Kv4Tile<D>::kBytes;
-  static constexpr bool kQRegs = D * NT <= 128;  // Q in registers (the batch of the header: 107 us, 112 from shared memory)
+  static constexpr bool kQRegs = D * NT <= 64;  // Q's high parts in registers (with d NT = 128 they pushed out others: 4 us)
   // ring of a warp: 9 KB, and twice that where 8 warps have an SM: 55 KB and more in flight (45 KB cover the latency)
   static constexpr int kStages = (D == 64 ? 4 : D == 128 ? 2 : 1) * (kBlocksPerSm * kWarps == 8 ? 2 : 1);
   static constexpr int kStageBytes = 2 * kTile;
-  static constexpr int kQBytes = NT * (D / 64) * 1024;  // [NT][D / 64][2][32] uint4
+  static constexpr int kPartBytes = NT * (D / 64) * 1024;  // high or low parts of Q: [NT][D / 64][2][32] uint4
   static constexpr int kInfoBytes = (kRows * (16 + 4 * (D / 64)) + 15) / 16 * 16;  // of the rows, see RowInfo
-  static constexpr int kWarpBytes = kStages * kStageBytes + kQBytes + kInfoBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kPartBytes + kInfoBytes;
   static constexpr int kSmem = kWarps * kWarpBytes;
   static_assert((kSmem + 5120) * kBlocksPerSm <= 228 * 1024, "shared memory of an SM");
 };
@@ -90,7 +89,7 @@ struct RowInfo {
   float back[ROWS];         // scores from sums of products
   int limit[ROWS];          // keys that the row sees
   long long out[ROWS];      // its O, in elements
-  float sums[GR][ROWS];     // of Q's entries, by group
+  float sums[GR][ROWS];     // of Q's entries, by group, times 2^-24
 };
 
 // Where a walk over a span's segments stands.
@@ -159,14 +158,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// d += a b of bytes, the warp's m16n8k32: a codes, b with a sign
-__device__ __forceinline__ void mma16832(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const int (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
-}
-
 // The codes of the low (high) byte of each half of w as float16 subnormals, code times 2^-24: n, the even
 // one, and b, even + 16 odd.
 __device__ __forceinline__ void low_codes(uint32_t w, uint32_t& n, uint32_t& b) {
@@ -207,8 +198,9 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * C::kWarpBytes;
-  uint4* sq = reinterpret_cast<uint4*>(ring + C::kStages * C::kStageBytes);
-  RowInfo<ROWS, GR>& info = *reinterpret_cast<RowInfo<ROWS, GR>*>(sq + C::kQBytes / 16);
+  uint4* shi = reinterpret_cast<uint4*>(ring + C::kStages * C::kStageBytes);
+  uint4* slo = shi + C::kPartBytes / 16;
+  RowInfo<ROWS, GR>& info = *reinterpret_cast<RowInfo<ROWS, GR>*>(slo + C::kPartBytes / 16);
   static_assert(sizeof(info) <= C::kInfoBytes, "room of the rows");
   uint64_t* bar = bars[warp];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
@@ -371,13 +363,13 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
     const int rows = min(ROWS, it.nq * p.G - row0);
 
     // Q, as the operand of row n = g (one of 8 per NT): lane (g, c) needs entries 16 c .. 16 c + 15 of every group.
-    // A lane here has 8 entries of a row.  Transformed in float32, then whole numbers of 16 bits, q = 256 high + low, with
-    // the row's largest entry at 32,639: two bytes with a sign.  Even and odd codes have their own, so the products
-    // with the codes are exact sums of whole numbers; a lane's 8 entries are one word each of high and low, even and odd.
-    // Entries are off by 2^-16 of the row's largest; the part of that along q goes back into the row's factor (|q|^2 over
-    // q times the rounded q): keys that weigh in lean towards q, so that is the part that would move LSE most.
-    // (Two float16 of q instead took twice the products: the batch of the header 115 us; one of them 103, but LSE was off
-    // by 3e-6 of itself.)
+    // A lane here has 8 entries of a row.  Transformed in float32, scaled by a power of two that puts the row's
+    // largest entry at 2^13 .. 2^14 (back takes it back, and the 2^-24 of the codes).
+    // A byte of codes is b = even + 16 odd, so with cb = q_odd / 16 and cn = q_even - cb the products
+    // cn even + cb b are q_even even + q_odd odd.  Both are kept as two float16, the rounded value and what its
+    // rounding left (22 bits: bf16 rows are exact, transformed rows as near as float32 sums).  With the rounded values
+    // alone the batch of the header takes 103 us, but LSE is off by 3e-6 of itself instead of 3e-7; with q in whole
+    // numbers of 16 bits and integer products 107, but of few keys LSE is off by 2e-5.
     if (seg_no > 0) {
       mates = 1u << warp;
       set = 0, set_step = 1;
@@ -391,7 +383,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
 #pragma unroll 1
       for (; set < ROWS / kAtOnce; set += set_step) {
         const int n = set * kAtOnce + sub;
-        uint4 ops = make_uint4(0u, 0u, 0u, 0u);  // high and low of the even entries, of the odd ones
+        uint4 high = make_uint4(0u, 0u, 0u, 0u), low = high;
         float back = 0.f, sum = 0.f;
         if (set * kAtOnce < rows) {
           float x[8];
@@ -424,46 +416,37 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
           }
           float top = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
 #pragma unroll
-          for (int st = 1; st < kLanes; st <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, st));
-          // 2^-ex brings any finite row into range; a row with an infinity or NaN gets a factor that is not finite
+          for (int st = 1; st < kLanes; st <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, st));
           const int ex = top > 0.f ? min(max(exponent_of(top) - 13, -100), 100) : 0;
-          const float f = exp2_int(-ex), most = top * f;
-          const float inv = most > 0.f ? 32639.f / most : 0.f, unit = most * (1.f / 32639.f);
-          float along[2] = {0.f, 0.f};
-          int isum = 0;
-          uint32_t bytes[4] = {0u, 0u, 0u, 0u};
+          const float f = exp2_int(-ex);
+          float hn[4], hb[4], ln[4], lb[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = x[j] * f;
-            const int v = __float2int_rn(a * inv), high = (v + 128) >> 8;
-            along[0] = fmaf(a, a, along[0]);
-            along[1] = fmaf(a, static_cast<float>(v), along[1]);
-            isum += v;
-            bytes[2 * (j & 1)] |= (static_cast<uint32_t>(high) & 255u) << (8 * (j >> 1));
-            bytes[2 * (j & 1) + 1] |= (static_cast<uint32_t>(v) & 255u) << (8 * (j >> 1));
+          for (int j = 0; j < 4; ++j) {
+            const float cb = x[2 * j + 1] * f * 0.0625f, cn = x[2 * j] * f - cb;
+            hb[j] = __half2float(__float2half_rn(cb));
+            lb[j] = __half2float(__float2half_rn(cb - hb[j]));
+            hn[j] = __half2float(__float2half_rn(cn));
+            ln[j] = __half2float(__float2half_rn(cn - hn[j]));
+            sum += (hn[j] + ln[j]) + 17.f * (hb[j] + lb[j]);
           }
-          ops = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
 #pragma unroll
-          for (int st = 1; st < 8; st <<= 1) isum += __shfl_xor_sync(0xffffffffu, isum, st);
-          sum = static_cast<float>(isum);
-#pragma unroll
-          for (int st = 1; st < kLanes; st <<= 1) {
-            along[0] += __shfl_xor_sync(0xffffffffu, along[0], st);
-            along[1] += __shfl_xor_sync(0xffffffffu, along[1], st);
-          }
-          const float ratio = along[0] / (along[1] * unit);
-          const float keep = fabsf(ratio - 1.f) < 0.01f ? ratio : 1.f;  // not for rows of zeros, infinities or NaN
-          back = p.scale_log2 * exp2_int(ex) * unit * keep;
+          for (int st = 1; st < 8; st <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, st);
+          sum *= 1.f / 16777216.f;
+          back = p.scale_log2 * exp2_int(ex) * 16777216.f;
+          high = make_uint4(pack_f16x2(hn[0], hn[2]), pack_f16x2(hb[0], hb[2]), pack_f16x2(hn[1], hn[3]), pack_f16x2(hb[1], hb[3]));
+          low = make_uint4(pack_f16x2(ln[0], ln[2]), pack_f16x2(lb[0], lb[2]), pack_f16x2(ln[1], ln[3]), pack_f16x2(lb[1], lb[3]));
         }
         const int r = row0 + n, i = r / p.G, hq = h * p.G + r - i * p.G;
         const int limit = p.causal && n < rows ? min(nk, see0 + i) : nk;
         const long long out = (q0 + i) * p.o_sn + hq * p.o_sh;
         for (unsigned m = mates; m; m &= m - 1) {
           uint8_t* const of = smem + (__ffs(m) - 1) * C::kWarpBytes + C::kStages * C::kStageBytes;
-          reinterpret_cast<uint4*>(of)[to + (n / 8 * GR * 2) * 32 + 4 * (n % 8)] = ops;
-          RowInfo<ROWS, GR>& inf = *reinterpret_cast<RowInfo<ROWS, GR>*>(of + C::kQBytes);
+          uint4* const dst = reinterpret_cast<uint4*>(of) + to + (n / 8 * GR * 2) * 32 + 4 * (n % 8);
+          dst[0] = high;
+          dst[C::kPartBytes / 16] = low;
+          RowInfo<ROWS, GR>& inf = *reinterpret_cast<RowInfo<ROWS, GR>*>(of + 2 * C::kPartBytes);
           if (oct == 0) inf.back[n] = back, inf.limit[n] = limit, inf.out[n] = out;
           if ((oct & 7) == 0) inf.sums[gr][n] = sum;
         }
@@ -484,7 +467,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
         for (int e = 0; e < 2; ++e) qs[nt][gr][e] = info.sums[gr][8 * nt + 2 * c + e];
         if constexpr (C::kQRegs)
 #pragma unroll
-          for (int kp = 0; kp < 2; ++kp) qf[nt][gr][kp] = sq[((nt * GR + gr) * 2 + kp) * 32 + lane];
+          for (int kp = 0; kp < 2; ++kp) qf[nt][gr][kp] = shi[((nt * GR + gr) * 2 + kp) * 32 + lane];
       }
     }
     const int min_lim = p.causal ? min(it.nk, max(0, it.nk - it.nq + row0 / p.G + 1)) : it.nk;
@@ -560,31 +543,32 @@ __global__ void __launch_bounds__(SplitCfg<D, NT>::kThreads, SplitCfg<D, NT>::kB
           for (int gp = 0; gp < F::kGroups; ++gp) {
             const int gr = pl * F::kGroups + gp;
             float acc[2][NT][4];
-            uint4 q0[NT], q1[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (C::kQRegs) {
-                q0[nt] = qf[nt][gr][0], q1[nt] = qf[nt][gr][1];
-              } else {
-                q0[nt] = sq[(nt * GR + gr) * 64 + lane], q1[nt] = sq[(nt * GR + gr) * 64 + 32 + lane];
-              }
-            }
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti) {
-              const uint32_t w[4] = {wa[ti][2 * gp], wb[ti][2 * gp], wa[ti][2 * gp + 1], wb[ti][2 * gp + 1]};
-              uint32_t even[4], odd[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) even[i] = w[i] & 0x0F0F0F0Fu, odd[i] = (w[i] >> 4) & 0x0F0F0F0Fu;
+            for (int kp = 0; kp < 2; ++kp) {
+              uint4 hi[NT], lo[NT];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                constexpr int zero[4] = {0, 0, 0, 0};
-                int high[4], low[4];
-                mma16832(high, even, q0[nt].x, q1[nt].x, zero);
-                mma16832(low, even, q0[nt].y, q1[nt].y, zero);
-                mma16832(high, odd, q0[nt].z, q1[nt].z, high);
-                mma16832(low, odd, q0[nt].w, q1[nt].w, low);
+                if constexpr (C::kQRegs) hi[nt] = qf[nt][gr][kp];
+                else hi[nt] = shi[((nt * GR + gr) * 2 + kp) * 32 + lane];
+                lo[nt] = slo[((nt * GR + gr) * 2 + kp) * 32 + lane];
+              }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[ti][nt][e] = static_cast<float>(high[e] * 256 + low[e]);
+              for (int ti = 0; ti < 2; ++ti) {
+                uint32_t f0[4], f1[4];
+                low_codes(wa[ti][2 * gp + kp], f0[0], f0[2]);
+                low_codes(wb[ti][2 * gp + kp], f0[1], f0[3]);
+                high_codes(wa[ti][2 * gp + kp], f1[0], f1[2]);
+                high_codes(wb[ti][2 * gp + kp], f1[1], f1[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&ac)[4] = acc[ti][nt];
+                  constexpr float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                  if (kp == 0) mma16816(ac, f0, hi[nt].x, hi[nt].y, zero);
+                  else mma16816(ac, f0, hi[nt].x, hi[nt].y, ac);
+                  mma16816(ac, f0, lo[nt].x, lo[nt].y, ac);
+                  mma16816(ac, f1, hi[nt].z, hi[nt].w, ac);
+                  mma16816(ac, f1, lo[nt].z, lo[nt].w, ac);
+                }
               }
             }
 #pragma unroll

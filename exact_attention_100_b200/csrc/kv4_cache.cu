@@ -38,6 +38,18 @@ __device__ __forceinline__ float bf16_up(float x) {  // x >= 0
   return __uint_as_float((__float_as_uint(x) + 0xFFFFu) & 0xFFFF0000u);
 }
 
+// minimum and maximum that a NaN goes through
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Rounds of a warp of the writer, up to 4 where there are enough rows for 4 blocks of threads on each of 148 processors
 // all the same (16,384 tokens of 8 heads of 128: 39.6, 32.1 and 28.6 us with 1, 2 and 4).
 constexpr int kAppendRounds = 4;

@@ -19,18 +19,6 @@ struct Kv4Tile {
   static constexpr int kSzRow = D / 16;                // bytes of the (s, z) pairs of one token
 };
 
-// minimum and maximum that a NaN goes through
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // First byte of the tile that holds slot `slot` of head h, and the slot's row in it.
 template <int D>
 __device__ __forceinline__ long long kv4_tile_offset(int block, int off, int page, int Hk, int h) {

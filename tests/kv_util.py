@@ -77,9 +77,8 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     A score s_j = scale q . k_j is off by at most d_j = scale e sum_i |q_i| |k_ji| + x |s_j| + x, with e the relative
     roundings of q's and k's entries and of the sums, x those of the scale factors and the exponential.
     LSE is then off by at most sum_j p_j d_j, O by sum_j p_j d_j |v_j - O|.
-    Few rows: codes and their products with q are exact; q's entries are rounded to whole numbers of 1/32639 of the row's
-    largest: off by r = 1.004 2^-16 max|q| each, and the row's factor is corrected by at most r sum|q| / sum q^2:
-    d_j gets scale r (sum_i |k_ji| + |q . k_j| sum|q| / sum q^2) more, and e = 2^-18 is for float32; x = 2^-20; p_j times
+    Few rows: q is kept in 22 bits and the codes are exact: e = 2^-21 + 2^-18 (float32 sums of up to 256 products
+    whose codes carry an offset, at most 16 times the value's own size, cut off at 2^-23 each), x = 2^-20; p_j times
     V's step is rounded by 2^-11, which moves O by 2^-11 sum_j p_j (|v_j| + 15 s_j) <= 2^-11 3 sum_j p_j max|v_j| (a code
     times its step is at most the range, twice the largest value).
     Many rows: q (transformed) and k are rounded to float16, 2^-11 each: e = 2^-10 + 2^-18, x as above, and the row's
@@ -96,7 +95,7 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     for b, n in enumerate(ctx):
         lo, hi = int(cu[b]), int(cu[b + 1])
         many = most > few and ((hi - lo) * group > few or len(ctx) == 1)
-        e, x = (2.0 ** -10 if many else 0) + 2.0 ** -18, 2.0 ** -20
+        e, x = (2.0 ** -10 if many else 2.0 ** -21) + 2.0 ** -18, 2.0 ** -20
         for h in range(q.shape[1]):
             kh = h // group
             for i in range(lo, hi):
@@ -110,10 +109,6 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
                 dj = scale * e * (np.abs(k) @ np.abs(q[i, h])) + x * np.abs(s) + x
                 if many:
                     dj += 2.0 ** -11 * np.abs(s)
-                else:
-                    a = np.abs(q[i, h])
-                    r = 1.004 * 2.0 ** -16 * a.max()
-                    dj += scale * r * np.abs(k).sum(-1) + np.abs(s) * r * a.sum() / max((a * a).sum(), 1e-300)
                 vmax = np.abs(v).max(-1, keepdims=True)
                 round_p = 3 * 2.0 ** -11 * (p @ np.abs(v)) if many else 2.0 ** -11 * 3 * (p @ vmax)
                 ob[i, h] = 1.1 * ((p * dj) @ np.abs(v - o_ref[i, h]) + round_p) + 2.0 ** -8 * np.abs(o_ref[i, h])
