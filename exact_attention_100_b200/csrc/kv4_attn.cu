@@ -59,6 +59,10 @@ constexpr int kChunkCost = 5;
 // for 32 rows, 104 and 112 for 48, 134 and 113 for 64; d = 64: 66 and 96 for 48, 83 and 97 for 64, 118 and 96 for 96;
 // d = 256: 106 and 140 for 24, 136 and 141 for 32, 165 and 140 for 40.
 constexpr int chunk_min_rows(int d) { return d == 64 ? 64 : d == 128 ? 48 : 32; }
+// So do those of fewer keys than this, whatever their rows, stay here if Q is transformed: the chunk kernel rounds it to
+// float16, and over few keys that does not average out (LSE off by 9e-6 of itself for 64 to 138 queries over 64 to 351
+// keys, by 5e-7 over thousands)
+constexpr int kChunkMinKeys = 128;
 // Units after which the sums of codes are centred
 constexpr int kCentre = 16;
 
@@ -909,14 +913,18 @@ cudaError_t setup_kv4_attn_kernels() {
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int d, int num_sms, cudaStream_t stream, int* launches) {
   Kv4AttnParams few = p;
   *launches = 2;
-  if (may_chunk(p.max_q, p.G, d)) {
-    // requests of many rows go to the chunk kernel, the others of the batch, if it has any, to this one; both
-    // write their parts into the same workspace, one after the other
-    Kv4AttnParams many = p;
-    many.min_rows = few.max_rows = p.B == 1 ? 0 : chunk_min_rows(d);  // a request alone: one kernel, whatever its rows
+  few.few_rows = chunk_min_rows(d);
+  few.few_keys = p.signs != nullptr ? kChunkMinKeys : 0;
+  if (may_chunk(p.max_q, p.G, d) && static_cast<long long>(p.width) * p.page >= few.few_keys) {
+    // requests of many rows and keys go to the chunk kernel, the others of the batch, if it may have any, to this one;
+    // both write their parts into the same workspace, one after the other
+    Kv4AttnParams many = few;
+    const bool alone = p.B == 1 && p.max_q >= few.few_keys;  // a request alone: one kernel, whatever its rows
+    many.take = alone ? 0 : 2;
+    few.take = 1;
     *launches = 3;
     const cudaError_t e = launch_kv4_chunk(many, d, num_sms, stream);
-    if (e != cudaSuccess || p.B == 1) return e;
+    if (e != cudaSuccess || alone) return e;
     *launches = 5;
   }
   // 8 rows on the small side of the products, or two sets of 8 for one pass over the keys where there

@@ -261,8 +261,7 @@ int attn_fwd_kv4(const void* q, const void* cache, const int* block_table, const
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 /
                                     (signs != nullptr ? std::sqrt(static_cast<double>(d)) : 1.0));
   p.causal = causal;
-  p.min_rows = 0;
-  p.max_rows = 0x7FFFFFFF;
+  p.take = 0;
   int launches = 0;
   if (ea::launch_kv4_attn(p, d, sms, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return ATTN_ERR_CUDA;
   ea::count_launches(launches);

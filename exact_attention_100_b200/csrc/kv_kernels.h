@@ -76,7 +76,9 @@ struct Kv4AttnParams {
   int B, Hq, Hk, G, total_q, max_q, width, page, num_blocks;
   float scale_log2;          // softmax scale * log2 e (times 1 / sqrt d with the transform)
   int causal;
-  int min_rows, max_rows;    // requests with min_rows < query length * G <= max_rows are this launch's
+  // Which requests are this launch's: 0 all of them, 1 those of few rows (query length * G at most few_rows) or few keys
+  // (below few_keys), 2 the others
+  int take, few_rows, few_keys;
 };
 // Bytes for any lengths of B requests with total_q queries, none longer than max_q.
 unsigned long long kv4_attn_workspace_bytes(int B, int Hk, int G, long long total_q, int max_q, int d, int num_sms);

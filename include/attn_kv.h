@@ -149,7 +149,7 @@ unsigned long long attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hk, int total
  *               overwritten; not shared by calls that may run at the same time.
  * Neither o nor lse may overlap any other array.
  * Arithmetic: softmax and sums in float32.  Requests of few rows (queries times Hq / Hk; up to 64 at d = 64, 48 at
- * d = 128, 32 at d = 256): the codes are multiplied as they are, Q in 22 bits (each row scaled by a power
+ * d = 128, 32 at d = 256) or, with signs, of fewer than 128 keys: the codes are multiplied as they are, Q in 22 bits (each row scaled by a power
  * of two), P times the step of V rounded to float16.  Others: Q (transformed), K, V and P rounded to float16 under
  * powers of two of their rows and blocks, so a score is off by 2^-10 of the sum of its products' sizes.
  * Work is split over keys by a rule on the lengths, and the parts are joined in a fixed order: results do

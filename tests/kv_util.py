@@ -66,8 +66,8 @@ def reference(q, ks, vs, cu, ctx, scale, causal, signs=None):
                              None if signs is None else signs.cpu().numpy())
 
 
-# Requests with more rows (queries times heads per key/value head) than this go to the kernel that brings K and V to
-# float16
+# Requests with more rows (queries times heads per key/value head) than this, and 128 keys if Q is transformed, go to
+# the kernel that brings K and V to float16
 FEW_ROWS = {64: 64, 128: 48, 256: 32}
 
 
@@ -94,7 +94,8 @@ def bounds(q, ks, vs, cu, ctx, scale, causal, signs, o_ref, lse_ref):
     most = max((int(cu[b + 1]) - int(cu[b])) * group for b in range(len(ctx)))
     for b, n in enumerate(ctx):
         lo, hi = int(cu[b]), int(cu[b + 1])
-        many = most > few and ((hi - lo) * group > few or len(ctx) == 1)
+        short = signs is not None and n < 128
+        many = most > few and ((hi - lo) * group > few and not short or len(ctx) == 1 and (signs is None or hi - lo >= 128))
         e, x = (2.0 ** -10 if many else 2.0 ** -21) + 2.0 ** -18, 2.0 ** -20
         for h in range(q.shape[1]):
             kh = h // group
